@@ -1,6 +1,7 @@
 // C ABI of the HiSparse swap-in path: argument checks, the pinned host pool, launches.
 #include "hisparse.h"
 #include "hs_internal.h"
+#include "hs_latent.h"
 
 #include <algorithm>
 #include <climits>
@@ -651,6 +652,236 @@ int hs_export_state(hs_ctx* ctx, void* d_dst, uint64_t dst_bytes, uint32_t what,
 
 int hs_import_state(hs_ctx* ctx, const void* d_src, uint64_t src_bytes, uint32_t what, void* stream) {
   return copy_state(ctx, const_cast<void*>(d_src), src_bytes, what, false, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int32_t kMaxTokens = 1 << 30;
+constexpr int32_t kMaxHeads = 512;
+
+int check_format(const hs_row_format* f, hs::RowLayout* l) {
+  if (!f) return fail(HS_E_INVALID, "row format is NULL");
+  if (f->latent != 256 && f->latent != 512)
+    return fail(HS_E_INVALID, "a row's latent part must have 256 or 512 values (got %d)", f->latent);
+  if (f->rope != 32 && f->rope != 64)
+    return fail(HS_E_INVALID, "a row's rope part must have 32 or 64 values (got %d)", f->rope);
+  if (f->type != HS_ROW_BF16 && f->type != HS_ROW_MXFP8)
+    return fail(HS_E_INVALID, "a row's type must be HS_ROW_BF16 (0) or HS_ROW_MXFP8 (1) (got %d)", f->type);
+  *l = hs::row_layout(f->latent, f->rope, f->type == HS_ROW_MXFP8);
+  return HS_OK;
+}
+
+// The format's layout, where the context's rows have its size.
+int check_rows(const hs_ctx* ctx, const hs_row_format* f, hs::RowLayout* l) {
+  const int rc = check_format(f, l);
+  if (rc) return rc;
+  if (l->bytes != ctx->cfg.row_bytes)
+    return fail(HS_E_INVALID, "rows of this format have %d bytes, the context's %d", l->bytes, ctx->cfg.row_bytes);
+  return HS_OK;
+}
+
+int check_heads(int32_t heads) {
+  if (heads < 1 || heads > kMaxHeads) return fail(HS_E_INVALID, "heads must be in [1, %d] (got %d)", kMaxHeads, heads);
+  return HS_OK;
+}
+
+int check_tokens(const char* name, int32_t n) {
+  if (n < 0 || n > kMaxTokens) return fail(HS_E_INVALID, "%s must be in [0, %d] (got %d)", name, kMaxTokens, n);
+  return HS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hs_row_bytes(const hs_row_format* fmt, int32_t* bytes) {
+  if (!bytes) return fail(HS_E_INVALID, "bytes output is NULL");
+  hs::RowLayout l;
+  const int rc = check_format(fmt, &l);
+  if (rc) return rc;
+  *bytes = l.bytes;
+  return ok();
+}
+
+int hs_map_tokens(hs_ctx* ctx, const int32_t* d_new, const int32_t* d_len, const int32_t* d_tail0, int32_t n_tokens,
+                  int32_t* d_cu, int32_t* d_req, int32_t* d_pos, int32_t* d_slot, int32_t* d_status, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  rc = check_tokens("n_tokens", n_tokens);
+  if (rc) return rc;
+  if (!d_new || !d_len || !d_cu) return fail(HS_E_INVALID, "new, len and cu must not be NULL");
+  if (n_tokens > 0 && (!d_req || !d_pos || !d_slot))
+    return fail(HS_E_INVALID, "req, pos and slot must not be NULL (n_tokens = %d)", n_tokens);
+  if (ctx->cfg.tail_tokens > 0 && !d_tail0)
+    return fail(HS_E_INVALID, "tail0 must not be NULL: the context has a tail (tail_tokens = %d)", ctx->cfg.tail_tokens);
+  if (ctx->cfg.tail_tokens == 0 && d_tail0)
+    return fail(HS_E_INVALID, "tail0 given but the context has no tail (tail_tokens = 0)");
+  hs::MapArgs a{};
+  a.R = ctx->cfg.num_requests;
+  a.B = ctx->cfg.device_buffer_size;
+  a.H = ctx->H;
+  a.T = ctx->cfg.tail_tokens;
+  a.n = n_tokens;
+  a.fresh = d_new;
+  a.len = d_len;
+  a.tail0 = d_tail0;
+  a.cu = d_cu;
+  a.req = d_req;
+  a.pos = d_pos;
+  a.slot = d_slot;
+  a.status = d_status;
+  hipError_t e = hs::launch_map(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "map launch");
+  return ok();
+}
+
+int hs_store_rows(hs_ctx* ctx, const hs_row_format* fmt, const void* d_x, int64_t x_stride, const void* d_weight,
+                  float eps, const double* d_freqs, int32_t rope_style, const int32_t* d_req, const int32_t* d_pos,
+                  const int32_t* d_slot, int32_t n_tokens, void* d_latent, int32_t* d_status, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  hs::StoreArgs a{};
+  rc = check_rows(ctx, fmt, &a.row);
+  if (rc) return rc;
+  rc = check_tokens("n_tokens", n_tokens);
+  if (rc) return rc;
+  if (rope_style != HS_ROPE_PAIRS && rope_style != HS_ROPE_HALVES)
+    return fail(HS_E_INVALID, "rope_style must be HS_ROPE_PAIRS (0) or HS_ROPE_HALVES (1) (got %d)", rope_style);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(HS_E_INVALID, "eps must be finite and >= 0 (got %g)", (double)eps);
+  if (n_tokens > 0 && (!d_x || !d_weight || !d_req || !d_pos || !d_slot))
+    return fail(HS_E_INVALID, "x, weight, req, pos and slot must not be NULL");
+  if (x_stride % 8 != 0 || x_stride < fmt->latent + fmt->rope)
+    return fail(HS_E_INVALID, "x_stride must be a multiple of 8 and at least %d (got %lld)", fmt->latent + fmt->rope,
+                (long long)x_stride);
+  if (!aligned(d_x, 16) || !aligned(d_weight, 16) || !aligned(d_latent, 16))
+    return fail(HS_E_INVALID, "x, weight and latent must be 16-byte aligned");
+  if (!aligned(d_freqs, 8)) return fail(HS_E_INVALID, "freqs must be 8-byte aligned");
+  a.R = ctx->cfg.num_requests;
+  a.B = ctx->cfg.device_buffer_size;
+  a.H = ctx->H;
+  a.T = ctx->cfg.tail_tokens;
+  a.n = n_tokens;
+  a.halves = rope_style == HS_ROPE_HALVES;
+  a.eps = eps;
+  a.x_stride = x_stride;
+  a.x = (const uint16_t*)d_x;
+  a.weight = (const uint16_t*)d_weight;
+  a.freqs = d_freqs;
+  a.req = d_req;
+  a.pos = d_pos;
+  a.slot = d_slot;
+  a.latent = (uint16_t*)d_latent;
+  a.status = d_status;
+  a.tail = (char*)ctx->views.tail;
+  a.hot = (char*)ctx->views.hot;
+  a.host = (char*)ctx->pool_dev;
+  a.page = ctx->views.page;
+  a.epoch = ctx->views.epoch;
+  hipError_t e = hs::launch_store(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "store launch");
+  return ok();
+}
+
+int hs_attend_work_bytes(const hs_config* cfg, const hs_row_format* fmt, int32_t heads, uint64_t* bytes) {
+  if (!bytes) return fail(HS_E_INVALID, "bytes output is NULL");
+  int32_t H;
+  hs::Layout L;
+  int rc = check_config(cfg, &H, &L);
+  if (rc) return rc;
+  hs::RowLayout row;
+  rc = check_format(fmt, &row);
+  if (rc) return rc;
+  if (row.bytes != cfg->row_bytes)
+    return fail(HS_E_INVALID, "rows of this format have %d bytes, the configuration's %d", row.bytes, cfg->row_bytes);
+  rc = check_heads(heads);
+  if (rc) return rc;
+  *bytes = hs::attend_work_bytes(cfg->num_requests, cfg->top_k, heads, row);
+  return ok();
+}
+
+int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t heads, float scale, const int32_t* d_out,
+              const void* d_gather, void* d_o, float* d_lse, void* d_work, uint64_t work_bytes, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  hs::AttendArgs a{};
+  rc = check_rows(ctx, fmt, &a.row);
+  if (rc) return rc;
+  rc = check_heads(heads);
+  if (rc) return rc;
+  if (!std::isfinite(scale)) return fail(HS_E_INVALID, "scale must be finite");
+  if (!d_q || !d_out || !d_o) return fail(HS_E_INVALID, "q, out and o must not be NULL");
+  if (!aligned(d_q, 16) || !aligned(d_o, 16) || !aligned(d_gather, 16) || !aligned(d_work, 16))
+    return fail(HS_E_INVALID, "q, o, gather and work must be 16-byte aligned");
+  a.R = ctx->cfg.num_requests;
+  a.k = ctx->cfg.top_k;
+  a.B = ctx->cfg.device_buffer_size;
+  a.T = ctx->cfg.tail_tokens;
+  a.heads = heads;
+  const uint64_t need = hs::attend_work_bytes(a.R, a.k, heads, a.row);
+  if (need > 0 && (!d_work || work_bytes < need))
+    return fail(HS_E_INVALID, "work buffer has %llu bytes, needs %llu", (unsigned long long)(d_work ? work_bytes : 0),
+                (unsigned long long)need);
+  a.splits = hs::attend_splits(a.R, a.k, heads, a.row);
+  a.scale = scale;
+  a.q = (const uint16_t*)d_q;
+  a.out = d_out;
+  a.hot = (const char*)ctx->views.hot;
+  a.tail = (const char*)ctx->views.tail;
+  a.gather = (const char*)d_gather;
+  a.o = (uint16_t*)d_o;
+  a.lse = d_lse;
+  a.work = (float*)d_work;
+  hipError_t e = hs::launch_attend(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "attend launch");
+  return ok();
+}
+
+int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void* d_rope, int64_t rope_stride,
+                     const int32_t* d_cu_q, const int32_t* d_cu_k, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope,
+                     int32_t rope, int32_t value, float scale, int32_t causal, void* d_o, float* d_lse, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  rc = check_heads(heads);
+  if (rc) return rc;
+  rc = check_tokens("n_q", n_q);
+  if (rc) return rc;
+  rc = check_tokens("n_k", n_k);
+  if (rc) return rc;
+  if (!((nope == 64 && value == 64) || (nope == 128 && value == 128) || (nope == 192 && value == 256)))
+    return fail(HS_E_INVALID, "(nope, value) must be (64, 64), (128, 128) or (192, 256) (got (%d, %d))", nope, value);
+  if (rope != 32 && rope != 64) return fail(HS_E_INVALID, "rope must be 32 or 64 (got %d)", rope);
+  if (!std::isfinite(scale)) return fail(HS_E_INVALID, "scale must be finite");
+  if (causal != 0 && causal != 1) return fail(HS_E_INVALID, "causal must be 0 or 1 (got %d)", causal);
+  if (!d_cu_q || !d_cu_k) return fail(HS_E_INVALID, "cu_q and cu_k must not be NULL");
+  if (n_q > 0 && (!d_q || !d_o)) return fail(HS_E_INVALID, "q and o must not be NULL");
+  if (n_k > 0 && (!d_kv || !d_rope)) return fail(HS_E_INVALID, "kv and rope must not be NULL");
+  if (n_k > 0 && (rope_stride % 8 != 0 || rope_stride < rope))
+    return fail(HS_E_INVALID, "rope_stride must be a multiple of 8 and at least %d (got %lld)", rope, (long long)rope_stride);
+  if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_rope, 16) || !aligned(d_o, 16))
+    return fail(HS_E_INVALID, "q, kv, rope and o must be 16-byte aligned");
+  hs::PromptArgs a{};
+  a.R = ctx->cfg.num_requests;
+  a.n_q = n_q;
+  a.n_k = n_k;
+  a.heads = heads;
+  a.nope = nope;
+  a.rope = rope;
+  a.value = value;
+  a.causal = causal;
+  a.rope_stride = rope_stride;
+  a.scale = scale;
+  a.q = (const uint16_t*)d_q;
+  a.kv = (const uint16_t*)d_kv;
+  a.krope = (const uint16_t*)d_rope;
+  a.cu_q = d_cu_q;
+  a.cu_k = d_cu_k;
+  a.o = (uint16_t*)d_o;
+  a.lse = d_lse;
+  hipError_t e = hs::launch_prompt(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "prompt launch");
+  return ok();
 }
 
 void hs_destroy(hs_ctx* ctx) {

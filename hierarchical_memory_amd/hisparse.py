@@ -21,10 +21,13 @@ HS_STATUS_BAD_ID, HS_STATUS_DUP_ID, HS_STATUS_BAD_STATE, HS_STATUS_STALE = 1, 2,
 HS_EVICT_LRU, HS_EVICT_FIFO = 0, 1
 HS_PLAN_ROW_SOURCES = 1
 HS_STATE_TABLES, HS_STATE_ROWS = 1, 2
+HS_ROW_BF16, HS_ROW_MXFP8 = 0, 1
+HS_ROPE_PAIRS, HS_ROPE_HALVES = 0, 1
 
 EXPORTED = ("hs_required_sizes", "hs_create", "hs_host_pool", "hs_bind_device", "hs_reset", "hs_resolve",
             "hs_plan", "hs_copy", "hs_trial", "hs_commit", "hs_offload", "hs_advance_tail", "hs_gather",
-            "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state", "hs_destroy", "hs_last_error")
+            "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state", "hs_row_bytes", "hs_map_tokens",
+            "hs_store_rows", "hs_attend_work_bytes", "hs_attend", "hs_attend_prompt", "hs_destroy", "hs_last_error")
 HS_STATIC_PLAN_BYTES = 8 << 20
 
 
@@ -55,6 +58,10 @@ class HsSizes(ctypes.Structure):
                 ("token_slot_table", ctypes.c_uint32), ("lds_bytes_rank", ctypes.c_uint32),
                 ("sparse_rank", ctypes.c_uint32), ("epoch_bytes", ctypes.c_uint64), ("state_tables_bytes", ctypes.c_uint64),
                 ("state_rows_bytes", ctypes.c_uint64)]
+
+
+class HsRowFormat(ctypes.Structure):
+    _fields_ = [("latent", ctypes.c_int32), ("rope", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -90,13 +97,21 @@ def lib():
         L.hs_advance_tail.argtypes = [vp, vp, vp, vp, vp]
         L.hs_gather.argtypes = [vp, vp, vp, vp]
         L.hs_rebuild_order.argtypes = [vp, vp]
+        fmt, f32, i64 = ctypes.POINTER(HsRowFormat), ctypes.c_float, ctypes.c_int64
+        L.hs_row_bytes.argtypes = [fmt, ctypes.POINTER(i32)]
+        L.hs_map_tokens.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+        L.hs_store_rows.argtypes = [vp, fmt, vp, i64, vp, f32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
+        L.hs_attend_work_bytes.argtypes = [ctypes.POINTER(HsConfig), fmt, i32, ctypes.POINTER(ctypes.c_uint64)]
+        L.hs_attend.argtypes = [vp, fmt, vp, i32, f32, vp, vp, vp, vp, vp, ctypes.c_uint64, vp]
+        L.hs_attend_prompt.argtypes = [vp, vp, vp, vp, i64, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp]
         L.hs_destroy.argtypes = [vp]
         L.hs_destroy.restype = None
         L.hs_last_error.argtypes = []
         L.hs_last_error.restype = ctypes.c_char_p
         for name in ("hs_required_sizes", "hs_create", "hs_host_pool", "hs_bind_device", "hs_reset", "hs_resolve",
                      "hs_plan", "hs_copy", "hs_trial", "hs_commit", "hs_offload", "hs_advance_tail", "hs_gather",
-                     "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state"):
+                     "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state", "hs_row_bytes",
+                     "hs_map_tokens", "hs_store_rows", "hs_attend_work_bytes", "hs_attend", "hs_attend_prompt"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -346,6 +361,131 @@ def hs_import_state(ctx, src, what: int = 3, stream=None) -> None:
     _check(lib().hs_import_state(ctx, p, _bytes(src), what, _stream(stream)))
 
 
+def row_format(latent: int = 512, rope: int = 64, row_type: int = HS_ROW_BF16) -> HsRowFormat:
+    """Format of the latent rows: latent values, rope values, HS_ROW_BF16 or HS_ROW_MXFP8."""
+    return HsRowFormat(latent, rope, row_type)
+
+
+def hs_row_bytes(fmt: HsRowFormat) -> int:
+    n = ctypes.c_int32()
+    _check(lib().hs_row_bytes(ctypes.byref(fmt), ctypes.byref(n)))
+    return n.value
+
+
+def _on_device(*tensors) -> None:
+    """Refuses a tensor of another GPU than the current one (the library checks that this is the context's)."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"expected a tensor on the current device (cuda:{dev}), got one on {t.device}")
+
+
+def _typed(name: str, t, dtype, shape=None, nullable: bool = False):
+    """A contiguous tensor argument of one dtype and shape (None in the shape: any size), or None where it may be."""
+    if t is None:
+        if nullable:
+            return None
+        raise ValueError(f"{name} must not be None")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor, got {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def hs_map_tokens(ctx, new, length, tail0, cu, req, pos, slot, status=None, stream=None) -> None:
+    """new, length: device int32 [R], new and present tokens of each request; tail0 [R] where the context has a tail,
+    else None. Outputs: cu [R + 1], and req, pos, slot of one length, the most tokens that the map takes."""
+    lim = _lim(ctx)
+    R = lim.R if lim is not None else 0
+    n = req.numel() if req is not None else 0
+    for name, t in (("pos", pos), ("slot", slot)):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"req and {name} must have one length, got {n} and {t.numel()}")
+    _on_device(new, length, tail0, cu, req, pos, slot, status)
+    a = _ptrs(_arg("new", new, lim, R), _arg("length", length, lim, R), _arg("tail0", tail0, lim, R, nullable=True),
+              _arg("cu", cu, lim, R + 1), _arg("req", req, lim), _arg("pos", pos, lim), _arg("slot", slot, lim),
+              _arg("status", status, lim, R, nullable=True))
+    _check(lib().hs_map_tokens(ctx, *a[:3], n, *a[3:], _stream(stream)))
+
+
+def hs_store_rows(ctx, fmt: HsRowFormat, x, weight, eps: float, freqs, req, pos, slot, latent=None,
+                  rope_style: int = HS_ROPE_PAIRS, status=None, stream=None) -> None:
+    """x: device bf16 [n, latent + rope], rows of any stride that is a multiple of 8 (a slice of a wider projection);
+    weight: bf16 [latent]; freqs: float64 [rope / 2] or None; req, pos, slot: int32 [n] as hs_map_tokens wrote them;
+    latent: bf16 [n, latent + rope] output or None."""
+    import torch
+    lim = _lim(ctx)
+    _typed("x", x, torch.bfloat16, (None, fmt.latent + fmt.rope))
+    n = x.shape[0]
+    if x.stride(1) != 1:
+        raise ValueError("x must have contiguous rows")
+    _typed("weight", weight, torch.bfloat16, (fmt.latent,))
+    _typed("freqs", freqs, torch.float64, (fmt.rope // 2,), nullable=True)
+    _typed("latent", latent, torch.bfloat16, (n, fmt.latent + fmt.rope), nullable=True)
+    if not x.is_cuda:
+        raise ValueError(f"expected a GPU tensor, got one on {x.device}")
+    _on_device(x, weight, freqs, req, pos, slot, latent, status)
+    w, f, r, p, s, o, st = _ptrs(weight, freqs, _typed("req", req, torch.int32, (n,)),
+                                 _typed("pos", pos, torch.int32, (n,)), _typed("slot", slot, torch.int32, (n,)), latent,
+                                 _arg("status", status, lim, lim.R if lim is not None else 0, nullable=True))
+    _check(lib().hs_store_rows(ctx, ctypes.byref(fmt), x.data_ptr(), x.stride(0) if n > 1 else x.shape[1], w, eps, f,
+                               rope_style, r, p, s, n, o, st, _stream(stream)))
+
+
+def hs_attend_work_bytes(cfg: HsConfig, fmt: HsRowFormat, heads: int) -> int:
+    n = ctypes.c_uint64()
+    _check(lib().hs_attend_work_bytes(ctypes.byref(cfg), ctypes.byref(fmt), heads, ctypes.byref(n)))
+    return n.value
+
+
+def hs_attend(ctx, fmt: HsRowFormat, q, scale: float, out, o, lse=None, gather=None, work=None, stream=None) -> None:
+    """q: device bf16 [R, heads, latent + rope]; out: int32 [R, k] as a resolve or trial wrote it; gather: None (rows in
+    place) or the gathered rows; o: bf16 [R, heads, latent]; lse: float32 [R, heads] or None; work: a device buffer of
+    hs_attend_work_bytes."""
+    import torch
+    lim = _lim(ctx)
+    _typed("q", q, torch.bfloat16, (lim.R if lim is not None else None, None, fmt.latent + fmt.rope))
+    heads = q.shape[1]
+    _typed("o", o, torch.bfloat16, (q.shape[0], heads, fmt.latent))
+    _typed("lse", lse, torch.float32, (q.shape[0], heads), nullable=True)
+    _on_device(q, out, o, lse, gather, work)
+    a = _ptrs(q, _arg("out", out, lim, lim.RK if lim is not None else 0),
+              _arg("gather", gather, lim, nbytes=lim.gather if lim is not None else 0, int32=False, nullable=True),
+              o, lse, work)
+    _check(lib().hs_attend(ctx, ctypes.byref(fmt), a[0], heads, scale, *a[1:], _bytes(work), _stream(stream)))
+
+
+def hs_attend_prompt(ctx, q, kv, rope, cu_q, cu_k, scale: float, o, lse=None, causal: bool = True, stream=None) -> None:
+    """q: device bf16 [n_q, heads, nope + rope]; kv: bf16 [n_k, heads, nope + value]; rope: bf16 [n_k, rope], rows of
+    any stride that is a multiple of 8 (the rope columns of the latent rows); cu_q, cu_k: int32 [R + 1];
+    o: bf16 [n_q, heads, value]; lse: float32 [n_q, heads] or None."""
+    import torch
+    lim = _lim(ctx)
+    R = lim.R if lim is not None else 0
+    _typed("q", q, torch.bfloat16, (None, None, None))
+    n_q, heads, dq = q.shape
+    _typed("kv", kv, torch.bfloat16, (None, heads, None))
+    n_k = kv.shape[0]
+    _typed("rope", rope, torch.bfloat16, (n_k, None))
+    dr = rope.shape[1]
+    if rope.stride(1) != 1 and n_k > 0:
+        raise ValueError("rope must have contiguous rows")
+    _typed("o", o, torch.bfloat16, (n_q, heads, None))
+    value = o.shape[2]
+    nope = dq - dr
+    if kv.shape[2] != nope + value:
+        raise ValueError(f"kv must hold {nope} + {value} values a head (q's without rope, and o's), got {kv.shape[2]}")
+    _typed("lse", lse, torch.float32, (n_q, heads), nullable=True)
+    if not rope.is_cuda:
+        raise ValueError(f"expected a GPU tensor, got one on {rope.device}")
+    _on_device(q, kv, rope, cu_q, cu_k, o, lse)
+    pq, pkv, pcq, pck, po, pl = _ptrs(q, kv, _arg("cu_q", cu_q, lim, R + 1), _arg("cu_k", cu_k, lim, R + 1), o, lse)
+    _check(lib().hs_attend_prompt(ctx, pq, pkv, rope.data_ptr(), rope.stride(0) if n_k > 1 else dr, pcq, pck, n_q, n_k,
+                                  heads, nope, dr, value, scale, int(causal), po, pl, _stream(stream)))
+
+
 def hs_rebuild_order(ctx, stream=None) -> None:
     _check(lib().hs_rebuild_order(ctx, _stream(stream)))
 
@@ -422,6 +562,17 @@ class SwapIn:
     def plan_buffer(self):
         import torch
         return torch.empty((self.R, 4, self.k), dtype=torch.int32, device=self.device)
+
+    def map_buffers(self, n: int):
+        """Outputs of hs_map_tokens for up to n tokens: cu, req, pos, slot."""
+        import torch
+        return tuple(torch.empty((m,), dtype=torch.int32, device=self.device) for m in (self.R + 1, n, n, n))
+
+    def attend_work(self, fmt: HsRowFormat, heads: int):
+        """A work buffer for hs_attend (None where it takes none)."""
+        import torch
+        n = hs_attend_work_bytes(self.cfg, fmt, heads)
+        return torch.empty((n,), dtype=torch.uint8, device=self.device) if n else None
 
     def close(self) -> None:
         if self.ctx:

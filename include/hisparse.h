@@ -321,6 +321,119 @@ int hs_import_state(hs_ctx* ctx, const void* d_src, uint64_t src_bytes, uint32_t
  * with the rest). */
 int hs_rebuild_order(hs_ctx* ctx, void* stream);
 
+/*
+ * Latent attention over the rows: the operators around the swap-in step that turn a model's projections into
+ * rows and the selected rows into attention. A KV row of one token is the latent vector that every head's key
+ * and value are projections of, and a rotated part that every head's key shares ("HiSparse: Turbocharging Sparse
+ * Attention with Hierarchical Memory", section 2: a row per token, 576 bf16 = 512 latent + 64 rotated values).
+ *
+ * Row formats. latent is 256 or 512, rope 32 or 64:
+ *   HS_ROW_BF16   [latent bf16][rope bf16]
+ *   HS_ROW_MXFP8  [latent e4m3][latent / 32 scales e8m0, filled up to 16 bytes][rope bf16]: a latent value is its
+ *                 e4m3 value times 2^(b - 127), b the scale byte of its block of 32 (1 .. 254). A power-of-two
+ *                 scale keeps every value exact in bf16; it lies in the row because rows move one by one.
+ * The context's row_bytes must be hs_row_bytes of the format (1152 for 512 + 64 bf16 values, 656 in 8 bits).
+ */
+#define HS_ROW_BF16 0
+#define HS_ROW_MXFP8 1
+typedef struct hs_row_format {
+  int32_t latent; /* 256 or 512 */
+  int32_t rope;   /* 32 or 64 */
+  int32_t type;   /* HS_ROW_BF16 or HS_ROW_MXFP8 */
+} hs_row_format;
+
+/* Bytes of one row of a format. Host-only; HS_E_INVALID for a format that is not offered. */
+int hs_row_bytes(const hs_row_format* fmt, int32_t* bytes);
+
+/*
+ * The map of a ragged batch of new tokens, from the requests' lengths alone, on the device.
+ *   d_new     [R] new tokens of each request (>= 0; a negative count is taken as 0 and sets HS_STATUS_BAD_ID)
+ *   d_len     [R] tokens that each request has already: its new tokens have positions d_len[r] + 0, 1, ...
+ *   d_tail0   [R] or NULL: first device-resident token of each request (as in hs_resolve); required exactly where
+ *             the context has a tail
+ *   n_tokens  entries of the per-token outputs (>= 0, at most 2^30). A batch may be shorter (the entries behind it
+ *             become -1, so a captured graph can replay one length) or longer (it is cut off there)
+ *   d_cu      [R + 1] start of each request's tokens in the packed batch, d_cu[R] their number (cut off at n_tokens)
+ *   d_req     [n_tokens] request of each token, -1 behind the last
+ *   d_pos     [n_tokens] its position, -1 where it is not in [0, host_rows) or past the tail window's end
+ *   d_slot    [n_tokens] where its row goes: B + (pos mod T) inside the tail window [tail0, tail0 + T), else -1
+ *             (with pos >= 0: the host pool's row pos)
+ *   d_status  [R] or NULL: HS_STATUS_BAD_ID where one of the request's tokens (of those not cut off) got position
+ *             -1 or its count was negative, else 0
+ */
+int hs_map_tokens(hs_ctx* ctx, const int32_t* d_new, const int32_t* d_len, const int32_t* d_tail0, int32_t n_tokens,
+                  int32_t* d_cu, int32_t* d_req, int32_t* d_pos, int32_t* d_slot, int32_t* d_status, void* stream);
+
+/*
+ * New tokens' rows from the model's projection, written where the map says. For token t with request r, position
+ * x = d_pos[t] >= 0 and row input d_x[t * x_stride .. + latent + rope) (bf16):
+ *   y = latent part / sqrt(mean of its squares + eps) * d_weight (bf16 [latent]), in 32 bits
+ *   z = rope part with its pairs (HS_ROPE_PAIRS: (2i, 2i + 1), HS_ROPE_HALVES: (i, i + rope / 2)) turned by the angle
+ *       x * d_freqs[i] (radians, [rope / 2] double, 8-byte aligned; the angle is reduced in 64 bits, so positions of
+ *       any size turn exactly); d_freqs NULL: as they are
+ *   the row of the context's format from y and z, each value rounded once. HS_ROW_MXFP8: a block's scale is the least
+ *       power of two (at least 2^-100) that keeps it within 448.
+ * d_slot[t] in [B, B + T): the row becomes row d_slot[t] - B of the request's device tail. d_slot[t] == -1: it becomes
+ * host row x (over the host link), and replaces the row of a hot slot that holds the token, as hs_offload does; the
+ * request's change counter advances. Tokens with d_req or d_pos below 0 are skipped; one with another value out of
+ * range is skipped too and, where its request is one, sets HS_STATUS_BAD_ID in d_status[r] (optional; not written
+ * otherwise). Two tokens of one call must not name the same row.
+ * d_latent ([n_tokens][latent + rope] bf16, 16-byte aligned, or NULL) receives y and z in bf16 whatever the row format
+ * (what hs_attend_prompt reads its rope part from); rows of skipped tokens are left as they were.
+ * d_x must be 16-byte aligned and x_stride a multiple of 8, at least latent + rope. d_weight: 16-byte aligned.
+ * eps >= 0. n_tokens from 0 to 2^30. Rows of the tail that a trial or a copy on another stream reads must not be
+ * stored over meanwhile.
+ */
+#define HS_ROPE_PAIRS 0
+#define HS_ROPE_HALVES 1
+int hs_store_rows(hs_ctx* ctx, const hs_row_format* fmt, const void* d_x, int64_t x_stride, const void* d_weight,
+                  float eps, const double* d_freqs, int32_t rope_style, const int32_t* d_req, const int32_t* d_pos,
+                  const int32_t* d_slot, int32_t n_tokens, void* d_latent, int32_t* d_status, void* stream);
+
+/*
+ * One decode step's attention over the selected rows, absorbed form (every head's query already multiplied into the
+ * latent space): with the rows v_j = [latent | rope] of request r's selection,
+ *   s_hj = scale * q_h . v_j,   o_h = sum_j softmax_j(s_h)_j * latent part of v_j,   lse_h = ln sum_j exp(s_hj)
+ *   d_q       [R][heads][latent + rope] bf16, 16-byte aligned. heads: 1 .. 512
+ *   d_out     [R][k] row indices as hs_resolve, hs_plan + hs_copy or hs_trial wrote them: hot slot, B + tail row;
+ *             anything outside [0, B + T) (such as -1) is no row. The same index twice counts twice. With the split
+ *             step the copy must have completed (its new slots' rows are read).
+ *   d_gather  NULL: the rows are read in place from the hot buffer and the tail. Else [R][k][row_bytes], 16-byte aligned:
+ *             position i's row is d_gather[r][i] where d_out[r][i] names a row (a trial's rows, before any commit)
+ *   d_o       [R][heads][latent] bf16, 16-byte aligned; zeros for a request without a row
+ *   d_lse     [R][heads] float32 or NULL; -inf for a request without a row
+ *   d_work    hs_attend_work_bytes bytes of device memory, 16-byte aligned (NULL where that is 0), free again when the
+ *             call's work on the stream has completed. Calls that may overlap (two streams, two captured graphs) need
+ *             one each. Nothing in it has to start at zero.
+ * Scores, sums and partial results are held in 32 bits; the softmax weights are rounded to bf16 for the product
+ * with the rows (the sum that divides it is that of the rounded weights), the result once to bf16. The order of every sum is fixed, so equal inputs give equal bits. scale must
+ * be finite. Rows that are not selected are not read, so nothing in them reaches the result.
+ */
+int hs_attend_work_bytes(const hs_config* cfg, const hs_row_format* fmt, int32_t heads, uint64_t* bytes);
+int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t heads, float scale, const int32_t* d_out,
+              const void* d_gather, void* d_o, float* d_lse, void* d_work, uint64_t work_bytes, void* stream);
+
+/*
+ * A prompt's attention, expanded form, over the context's R requests as ragged sequences (packed as hs_map_tokens
+ * numbers them). Head h of key token j has the key [kv[j][h][0 .. nope) | rope part of token j] and the value
+ * kv[j][h][nope .. nope + value): kv is the product of the latent rows with each head's up-projections, as one matrix
+ * product leaves it, and the rope part, shared by all heads, is read from the latent rows themselves.
+ *   d_q     [n_q][heads][nope + rope] bf16;  d_kv [n_k][heads][nope + value] bf16;  both 16-byte aligned
+ *   d_rope  rope values of key token j at d_rope + j * rope_stride elements (16-byte aligned, stride a multiple of 8)
+ *   d_cu_q, d_cu_k  [R + 1] starts of each request's queries and keys, ascending from 0 (values are cut to
+ *           [0, n_q] and [0, n_k]; a request whose end lies before its start has none; a query row that two requests
+           name gets either's result)
+ *   causal  1: query i of a request with m queries and n keys sees its first n - m + i + 1 keys (the queries are the last
+ *           m tokens); 0: all n
+ *   d_o     [n_q][heads][value] bf16, 16-byte aligned;  d_lse [n_q][heads] float32 or NULL. Zeros and -inf for a query
+ *           that sees no key. Rows behind the last request are left as they were.
+ * heads: 1 .. 512; (nope, value) one of (64, 64), (128, 128), (192, 256); rope 32 or 64; n_q, n_k from 0 to 2^30.
+ * Precision as in hs_attend.
+ */
+int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void* d_rope, int64_t rope_stride,
+                     const int32_t* d_cu_q, const int32_t* d_cu_k, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope,
+                     int32_t rope, int32_t value, float scale, int32_t causal, void* d_o, float* d_lse, void* stream);
+
 /* Free the host pool and the context (device buffers belong to the caller). NULL is ignored. */
 void hs_destroy(hs_ctx* ctx);
 
