@@ -207,6 +207,8 @@ int hs_create(const hs_config* cfg, hs_ctx** out) {
   // the most any context may use, so a later context of a smaller shape cannot lower it under this one.
   e = hs::set_lds_limits(cap, cap);
   if (e != hipSuccess) return hip_fail(e, "hipFuncSetAttribute(resolve kernel LDS)");
+  e = hs::set_attend_lds();
+  if (e != hipSuccess) return hip_fail(e, "hipFuncSetAttribute(attention kernel LDS)");
   {
     std::lock_guard<std::mutex> lock(g_static_plan_mu);
     if ((int)g_static_plan.size() <= dev) g_static_plan.resize((size_t)dev + 1, nullptr);

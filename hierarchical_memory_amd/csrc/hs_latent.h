@@ -94,6 +94,9 @@ struct PromptArgs {
 int attend_splits(int R, int k, int heads, const RowLayout& row);
 uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row);
 
+// Allows the attention kernels the LDS that they take, on the current device.
+hipError_t set_attend_lds();
+
 hipError_t launch_map(const MapArgs& a, hipStream_t s);
 hipError_t launch_store(const StoreArgs& a, hipStream_t s);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s);
