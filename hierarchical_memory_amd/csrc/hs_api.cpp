@@ -208,6 +208,7 @@ int hs_create(const hs_config* cfg, hs_ctx** out) {
   e = hs::set_lds_limits(cap, cap);
   if (e != hipSuccess) return hip_fail(e, "hipFuncSetAttribute(resolve kernel LDS)");
   e = hs::set_attend_lds();
+  if (e == hipSuccess) e = hs::set_prompt_lds();
   if (e != hipSuccess) return hip_fail(e, "hipFuncSetAttribute(attention kernel LDS)");
   {
     std::lock_guard<std::mutex> lock(g_static_plan_mu);
@@ -694,6 +695,19 @@ int check_tokens(const char* name, int32_t n) {
   return HS_OK;
 }
 
+int check_prompt(int32_t n_q, int32_t n_k, int32_t heads, int32_t nope, int32_t rope, int32_t value) {
+  int rc = check_heads(heads);
+  if (rc) return rc;
+  rc = check_tokens("n_q", n_q);
+  if (rc) return rc;
+  rc = check_tokens("n_k", n_k);
+  if (rc) return rc;
+  if (!((nope == 64 && value == 64) || (nope == 128 && value == 128) || (nope == 192 && value == 256)))
+    return fail(HS_E_INVALID, "(nope, value) must be (64, 64), (128, 128) or (192, 256) (got (%d, %d))", nope, value);
+  if (rope != 32 && rope != 64) return fail(HS_E_INVALID, "rope must be 32 or 64 (got %d)", rope);
+  return HS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -840,20 +854,25 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
   return ok();
 }
 
+int hs_attend_prompt_work_bytes(int32_t num_requests, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope, int32_t rope,
+                                int32_t value, uint64_t* bytes) {
+  if (!bytes) return fail(HS_E_INVALID, "bytes output is NULL");
+  if (num_requests < 1 || num_requests > 65535)
+    return fail(HS_E_INVALID, "num_requests must be in [1, 65535] (got %d)", num_requests);
+  const int rc = check_prompt(n_q, n_k, heads, nope, rope, value);
+  if (rc) return rc;
+  *bytes = hs::prompt_work_bytes(num_requests, n_q, n_k, heads, value);
+  return ok();
+}
+
 int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void* d_rope, int64_t rope_stride,
                      const int32_t* d_cu_q, const int32_t* d_cu_k, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope,
-                     int32_t rope, int32_t value, float scale, int32_t causal, void* d_o, float* d_lse, void* stream) {
+                     int32_t rope, int32_t value, float scale, int32_t causal, void* d_o, float* d_lse, void* d_work,
+                     uint64_t work_bytes, void* stream) {
   int rc = check_ready(ctx);
   if (rc) return rc;
-  rc = check_heads(heads);
+  rc = check_prompt(n_q, n_k, heads, nope, rope, value);
   if (rc) return rc;
-  rc = check_tokens("n_q", n_q);
-  if (rc) return rc;
-  rc = check_tokens("n_k", n_k);
-  if (rc) return rc;
-  if (!((nope == 64 && value == 64) || (nope == 128 && value == 128) || (nope == 192 && value == 256)))
-    return fail(HS_E_INVALID, "(nope, value) must be (64, 64), (128, 128) or (192, 256) (got (%d, %d))", nope, value);
-  if (rope != 32 && rope != 64) return fail(HS_E_INVALID, "rope must be 32 or 64 (got %d)", rope);
   if (!std::isfinite(scale)) return fail(HS_E_INVALID, "scale must be finite");
   if (causal != 0 && causal != 1) return fail(HS_E_INVALID, "causal must be 0 or 1 (got %d)", causal);
   if (!d_cu_q || !d_cu_k) return fail(HS_E_INVALID, "cu_q and cu_k must not be NULL");
@@ -861,8 +880,12 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
   if (n_k > 0 && (!d_kv || !d_rope)) return fail(HS_E_INVALID, "kv and rope must not be NULL");
   if (n_k > 0 && (rope_stride % 8 != 0 || rope_stride < rope))
     return fail(HS_E_INVALID, "rope_stride must be a multiple of 8 and at least %d (got %lld)", rope, (long long)rope_stride);
-  if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_rope, 16) || !aligned(d_o, 16))
-    return fail(HS_E_INVALID, "q, kv, rope and o must be 16-byte aligned");
+  if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_rope, 16) || !aligned(d_o, 16) || !aligned(d_work, 16))
+    return fail(HS_E_INVALID, "q, kv, rope, o and work must be 16-byte aligned");
+  const uint64_t need = hs::prompt_work_bytes(ctx->cfg.num_requests, n_q, n_k, heads, value);
+  if (need > 0 && (!d_work || work_bytes < need))
+    return fail(HS_E_INVALID, "work buffer has %llu bytes, needs %llu", (unsigned long long)(d_work ? work_bytes : 0),
+                (unsigned long long)need);
   hs::PromptArgs a{};
   a.R = ctx->cfg.num_requests;
   a.n_q = n_q;
@@ -877,6 +900,8 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
   a.q = (const uint16_t*)d_q;
   a.kv = (const uint16_t*)d_kv;
   a.krope = (const uint16_t*)d_rope;
+  a.splits = hs::prompt_splits(a.R, n_q, n_k, heads, value);
+  a.work = (float*)d_work;
   a.cu_q = d_cu_q;
   a.cu_k = d_cu_k;
   a.o = (uint16_t*)d_o;

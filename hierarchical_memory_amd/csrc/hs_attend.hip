@@ -12,6 +12,7 @@
 // never change lanes). With w head groups of 32 the other 4 / w waves of a group share out the latent dimensions of the
 // second product and each repeat the first.
 #include "hs_latent.h"
+#include "hs_mfma.h"
 
 #include <climits>
 #include <utility>
@@ -20,49 +21,12 @@ namespace hs {
 
 namespace {
 
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-typedef short s4 __attribute__((ext_vector_type(4)));
-typedef float f16 __attribute__((ext_vector_type(16)));
-typedef float f4 __attribute__((ext_vector_type(4)));
-#define HS_LDS __attribute__((address_space(3)))
-#define HS_GLOBAL __attribute__((address_space(1)))
-
 constexpr int kAttendThreads = 256;
 constexpr int kTile = 32;          // rows of a tile
 constexpr int kDepth = 4;          // tiles in LDS as memory has them: one in use, the others on their way
 constexpr int kListed = 1024;      // rows of the selection whose indices are held in LDS at a time
 constexpr int kGroupHeads = 128;   // most heads of one workgroup
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum moves only when a score passes it by more than this (in powers of two): weights above one are as
-// exact (bf16 has the exponents of 32 bits, and only ratios count), and moving it means touching every accumulator.
-constexpr float kSlack = 16.0f;
-
 __device__ __align__(16) uint4 zero_row[72];  // what a tile holds where there is no row
-
-// The tiles' loads go from memory to LDS past the registers, and past the compiler: it would wait for all of them before
-// any read of LDS. They are counted here instead. Loads end in their order, so N or fewer on their way means that the
-// older ones are in LDS; the wave's own LDS reads have ended too when it passes.
-template <int N>
-__device__ __forceinline__ void wait_loads_and_meet() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// 16 bytes of each lane's address + kOffset to LDS at lds + 16 * lane (the instruction adds its offset to both).
-template <int kOffset>
-__device__ __forceinline__ void load_to_lds(const char* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds - kOffset), "v"(p),
-               "n"(kOffset)
-               : "memory", "m0");
-}
-
-// A tile in LDS: its rows' columns in groups of 64 values (128 bytes), one group of all rows after another, and the eight
-// 16-byte chunks of a group changing places by the row, so that neither reading eight rows at one chunk nor four rows at a
-// pair of chunks meets a bank twice. A wave's asynchronous load (16 bytes a lane, in order, into LDS) fills eight rows of
-// one group.
-__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
 template <int L, int P, bool kMx>
 struct Shape {
@@ -87,19 +51,6 @@ template <bool kHalf, int kGroupBytes, int... G>
 __device__ __forceinline__ void load_groups(const char* row, const char* last, uint32_t lds,
                                             std::integer_sequence<int, G...>) {
   (load_to_lds<128 * G>(kHalf && G == (int)sizeof...(G) - 1 ? last : row, lds + G * kGroupBytes), ...);
-}
-
-// The accumulators stay in the matrix unit's half of the registers, which other instructions do not reach: one at a time
-// out, multiplied, and back. Seldom run.
-__device__ __forceinline__ void rescale(f16& o, float c) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float x = o[i], y;
-    asm("s_nop 7\n\tv_accvgpr_read_b32 %1, %0\n\ts_nop 1\n\tv_mul_f32 %1, %1, %2\n\ts_nop 1\n\tv_accvgpr_write_b32 %0, %1\n\ts_nop 3"
-        : "+a"(x), "=&v"(y)
-        : "v"(c));
-    o[i] = x;
-  }
 }
 
 struct Part { int r, split, h0, begin, end; };
@@ -201,12 +152,8 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
   int kat[4], vat[2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) kat[i] = col * 128 + (((2 * i + half) ^ swizzle(col)) << 4);
-  {
-    const int key = 4 * half + ((lane & 15) >> 2), x = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      vat[i] = key * 128 + (((x ^ swizzle(key)) ^ (4 * i)) << 4) + 8 * (lane & 1) + S::kColBytes * (kBlocks / 2 * share);
-  }
+  for (int i = 0; i < 2; ++i) vat[i] = across_place(lane, i) + S::kColBytes * (kBlocks / 2 * share);
 
   const int tiles = (part.end - part.begin + kTile - 1) / kTile;
   auto write_list = [&](int from) {  // of the rows [from, from + kListed) of the part
@@ -316,10 +263,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
     for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const HS_LDS char* at = (const HS_LDS char*)(tile + vat[b & 1] + S::kColBytes * (b >> 1) + 2048 * j);
-        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)at);
-        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(at + 1024));
-        const bf8 v = __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        const bf8 v = read_across(tile + vat[b & 1] + S::kColBytes * (b >> 1) + 2048 * j);
         o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[j], o[b], 0, 0, 0);
       }
       if (b & 1) __builtin_amdgcn_sched_barrier(0);

@@ -88,14 +88,21 @@ struct PromptArgs {
   const int32_t* cu_k;    // [R + 1]
   uint16_t* o;            // [n_q][heads][value]
   float* lse;             // [n_q][heads] or nullptr
+  int32_t splits;         // parts of the keys, each a workgroup's
+  float* work;            // partial results where splits > 1
 };
 
 // Parts that hs_attend cuts a selection of k rows into, and the bytes of their partial results.
 int attend_splits(int R, int k, int heads, const RowLayout& row);
 uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row);
 
+// The same for hs_attend_prompt: parts of every query tile's keys.
+int prompt_splits(int R, int n_q, int n_k, int heads, int value);
+uint64_t prompt_work_bytes(int R, int n_q, int n_k, int heads, int value);
+
 // Allows the attention kernels the LDS that they take, on the current device.
 hipError_t set_attend_lds();
+hipError_t set_prompt_lds();
 
 hipError_t launch_map(const MapArgs& a, hipStream_t s);
 hipError_t launch_store(const StoreArgs& a, hipStream_t s);

@@ -1,0 +1,73 @@
+// What the two attention kernels share: types, loads past the registers into LDS, LDS places, accumulators (gfx950).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hs {
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef float f16 __attribute__((ext_vector_type(16)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+#define HS_LDS __attribute__((address_space(3)))
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum moves only when a score passes it by more than this (in powers of two): weights above one are as
+// exact (bf16 has the exponents of 32 bits, and only ratios count), and moving it means touching every accumulator.
+constexpr float kSlack = 16.0f;
+
+// The tiles' loads go from memory to LDS past the registers, and past the compiler: it would wait for all of them before
+// any read of LDS. They are counted here instead. Loads end in their order, so N or fewer on their way means that the
+// older ones are in LDS; the wave's own LDS reads have ended too when it passes.
+template <int N>
+__device__ __forceinline__ void wait_loads_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes of each lane's address + kOffset to LDS at lds + 16 * lane (the instruction adds its offset to both).
+template <int kOffset>
+__device__ __forceinline__ void load_to_lds(const char* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds - kOffset), "v"(p),
+               "n"(kOffset)
+               : "memory", "m0");
+}
+
+// A tile in LDS: its rows' columns in groups of 64 values (128 bytes), one group of all rows after another, and the eight
+// 16-byte chunks of a group changing places by the row, so that neither reading eight rows at one chunk nor four rows at a
+// pair of chunks meets a bank twice. A wave's asynchronous load (16 bytes a lane, in order, into LDS) fills eight rows of
+// one group.
+__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+
+// The accumulators stay in the matrix unit's half of the registers, which other instructions do not reach: one at a time
+// out, multiplied, and back. Seldom run.
+__device__ __forceinline__ void rescale(f16& o, float c) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x = o[i], y;
+    asm("s_nop 7\n\tv_accvgpr_read_b32 %1, %0\n\ts_nop 1\n\tv_mul_f32 %1, %1, %2\n\ts_nop 1\n\tv_accvgpr_write_b32 %0, %1\n\ts_nop 3"
+        : "+a"(x), "=&v"(y)
+        : "v"(c));
+    o[i] = x;
+  }
+}
+
+// The matrix unit's second operand read across a tile's rows: lane (column d = lane % 32 of the 32 that `at` begins) gets rows
+// 4 half + 0..3 and 8 + 4 half + 0..3 of the 16 that begin there, half = lane / 32.
+__device__ __forceinline__ bf8 read_across(const char* at) {
+  const HS_LDS char* p = (const HS_LDS char*)at;
+  const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)p);
+  const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(p + 1024));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Where read_across starts in a group of columns for this lane: its row and chunk, for the first and second 32 columns.
+__device__ __forceinline__ int across_place(int lane, int second) {
+  const int row = 4 * (lane >> 5) + ((lane & 15) >> 2), x = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+  return row * 128 + (((x ^ swizzle(row)) ^ (4 * second)) << 4) + 8 * (lane & 1);
+}
+
+}  // namespace hs

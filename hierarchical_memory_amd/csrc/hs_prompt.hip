@@ -1,79 +1,360 @@
-// A prompt's latent attention, expanded form, over ragged sequences (gfx950).
+// A prompt's latent attention, expanded form, over ragged sequences (gfx950): key j of head h is [kv_j,h nope part | rope
+// part of token j], its value the rest of kv_j,h.
+//
+//   s = scale * q . key,   o = sum_j p_j value_j / sum_j p_j,   p_j = 2^(s_j log2 e - m)   (m a running maximum)
+//
+// One pass over the keys, 64 to a tile, two tiles in LDS. A workgroup of four waves takes 128 (256) queries of one sequence
+// and head, 32 (64) to a wave. Matrix instructions do both products transposed, so that a query is a lane's column in both
+// and its maximum, sum and rescaling stay inside the lane:
+//   S^T[key][query]  = K Q^T     A: keys from LDS, B: the queries, kept in registers
+//   O^T[dim][query] += V^T P^T   A: values read through the transposing LDS load, B: the weights as S^T left them
+// (a lane half h holds the keys 8 i + 4 h + 0..3 of S^T; the second product takes its keys in that order).
 #include "hs_latent.h"
+#include "hs_mfma.h"
+
+#include <utility>
 
 namespace hs {
 
 namespace {
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
 constexpr int kPromptThreads = 256;
+constexpr int kPromptWaves = 4;
+constexpr int kKeys = 64;  // of a tile
+
+__device__ __align__(16) uint4 zero_key[64];  // what a tile holds behind the last key
+
+// DN, P: nope and rope values of a key, DV: of a value. kSets: column sets of 32 queries of a wave.
+template <int DN, int P, int DV, int kSets>
+struct PromptShape {
+  static constexpr int kQueries = 32 * kSets * kPromptWaves;
+  static constexpr int kSteps = (DN + P) / 16;
+  static constexpr int kKeyCols = DN / 64 + 1, kValueCols = DV / 64;  // groups of 64 columns (the last key group: rope)
+  static constexpr int kColBytes = kKeys * 128;
+  static constexpr int kTileBytes = (kKeyCols + kValueCols) * kColBytes;
+  static constexpr int kLoads = 2 * (kKeyCols + kValueCols);  // of a lane, for a tile
+  static constexpr uint32_t kLds = 2 * kTileBytes;
+};
 
 __device__ __forceinline__ int cut(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
-// One workgroup per query and head, in tiles of 256 keys.
-__global__ __launch_bounds__(kPromptThreads) void prompt_kernel(PromptArgs a) {
-  __shared__ float p[kPromptThreads], red[kPromptThreads];
-  __shared__ int seq;
-  const int tid = threadIdx.x, h = blockIdx.y;
-  const int D = a.nope + a.rope, K = a.nope + a.value;
-  for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
-    __syncthreads();
-    if (tid == 0) seq = -1;
-    __syncthreads();
-    for (int r = tid; r < a.R; r += kPromptThreads)
-      if (t >= cut(a.cu_q[r], a.n_q) && t < cut(a.cu_q[r + 1], a.n_q)) seq = r;
-    __syncthreads();
-    if (seq < 0) continue;
-    const int q1 = cut(a.cu_q[seq + 1], a.n_q);
-    const int k0 = cut(a.cu_k[seq], a.n_k), k1 = cut(a.cu_k[seq + 1], a.n_k);
-    int n = k1 - k0;
-    if (a.causal) n -= q1 - 1 - t;
-    if (n < 0) n = 0;
-    const uint16_t* q = a.q + ((size_t)t * a.heads + h) * D;
-    float m = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int j0 = 0; j0 < n; j0 += kPromptThreads) {
-      const int j = j0 + tid;
-      float s = -INFINITY;
-      if (j < n) {
-        const uint16_t* key = a.kv + ((size_t)(k0 + j) * a.heads + h) * K;
-        const uint16_t* kr = a.krope + (size_t)(k0 + j) * a.rope_stride;
-        s = 0.0f;
-        for (int d = 0; d < a.nope; ++d) s += bf(q[d]) * bf(key[d]);
-        for (int d = 0; d < a.rope; ++d) s += bf(q[a.nope + d]) * bf(kr[d]);
-        s *= a.scale;
-      }
-      red[tid] = s;
-      __syncthreads();
-      float top = m;
-      for (int i = 0; i < kPromptThreads; ++i) top = fmaxf(top, red[i]);
-      const float top0 = top == -INFINITY ? 0.0f : top;
-      const float c = __expf(m - top0);
-      p[tid] = __expf(s - top0);
-      __syncthreads();
-      l *= c;
-      o *= c;
-      for (int i = 0; i < kPromptThreads && j0 + i < n; ++i) {
-        l += p[i];
-        if (tid < a.value) o += p[i] * bf(a.kv[((size_t)(k0 + j0 + i) * a.heads + h) * K + a.nope + tid]);
-      }
-      m = top;
-      __syncthreads();
+// The sequence of query tile `id` and the tile's number in it: a scan over the sequences' tile counts, 256 at a time.
+template <int kQueries>
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int id, int* seq, int* tile, int* sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int before = 0;
+  for (int r0 = 0; r0 < a.R; r0 += kPromptThreads) {
+    const int r = r0 + tid;
+    int c = 0;
+    if (r < a.R) {
+      const int n = cut(a.cu_q[r + 1], a.n_q) - cut(a.cu_q[r], a.n_q);
+      c = n > 0 ? (n + kQueries - 1) / kQueries : 0;
     }
-    if (tid < a.value) {
-      __bf16 b = (__bf16)(l > 0.0f ? o / l : 0.0f);
-      a.o[((size_t)t * a.heads + h) * a.value + tid] = __builtin_bit_cast(uint16_t, b);
+    int x = c;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(x, d);
+      if (lane >= d) x += y;
     }
-    if (a.lse && tid == 0) a.lse[(size_t)t * a.heads + h] = m + logf(l);
+    if (lane == 63) sh[wave] = x;
+    if (tid == 0) sh[4] = -1;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kPromptWaves; ++w) {
+      if (w < wave) x += sh[w];
+      total += sh[w];
+    }
+    if (id >= before + x - c && id < before + x) {
+      sh[4] = r;
+      sh[5] = id - (before + x - c);
+    }
+    __syncthreads();
+    const int found = sh[4], at = sh[5];
+    __syncthreads();
+    if (found >= 0) {
+      *seq = __builtin_amdgcn_readfirstlane(found);
+      *tile = __builtin_amdgcn_readfirstlane(at);
+      return true;
+    }
+    before += total;
   }
+  return false;
+}
+
+template <int kBegin, int kGroupBytes, int... G>
+__device__ __forceinline__ void load_part(const char* row, uint32_t lds, std::integer_sequence<int, G...>) {
+  (load_to_lds<kBegin + 128 * G>(row, lds + G * kGroupBytes), ...);
+}
+
+template <int DN, int P, int DV, int kSets>
+__global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a, int slots) {
+  using S = PromptShape<DN, P, DV, kSets>;
+  constexpr int kBlocks = DV / 32;
+  extern __shared__ __align__(1024) char smem[];
+  __shared__ int sh[6];
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(HS_LDS char*)smem);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const int h = blockIdx.x % a.heads, split = blockIdx.x / a.heads;
+  int kat[4], vat[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) kat[i] = col * 128 + (((2 * i + half) ^ swizzle(col)) << 4);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) vat[i] = across_place(lane, i) + S::kKeyCols * S::kColBytes;
+  const float scale = fabsf(a.scale) * kLog2e;
+  const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale turns the queries round
+
+  for (int slot = blockIdx.y; slot < slots; slot += gridDim.y) {
+    // the last tiles of a sequence see the most keys, and go first
+    int seq, qt;
+    if (!find_tile<S::kQueries>(a, slots - 1 - slot, &seq, &qt, sh)) continue;
+    const int q0 = cut(a.cu_q[seq], a.n_q), nq = cut(a.cu_q[seq + 1], a.n_q) - q0;
+    const int k0 = cut(a.cu_k[seq], a.n_k);
+    int nk = cut(a.cu_k[seq + 1], a.n_k) - k0;
+    if (nk < 0) nk = 0;
+    const int first = qt * S::kQueries;
+    // keys that the workgroup's last query sees, and its part of their tiles
+    const int last_q = first + S::kQueries < nq ? first + S::kQueries - 1 : nq - 1;
+    const int end = a.causal ? cut(nk - nq + last_q + 1, nk) : nk;
+    const int all = (end + kKeys - 1) / kKeys;
+    const int t0 = (int)((int64_t)all * split / a.splits), t1 = (int)((int64_t)all * (split + 1) / a.splits);
+
+    const int wq = first + wave * 32 * kSets;  // the wave's first query
+    int limit[kSets];                           // keys that the lane's queries see
+    bf8 q[kSets][S::kSteps];
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+      const int i = wq + 32 * g + col, j = i < nq ? i : nq - 1;
+      limit[g] = a.causal ? cut(nk - nq + j + 1, nk) : nk;
+      const __bf16* src = (const __bf16*)a.q + ((size_t)(q0 + j) * a.heads + h) * (DN + P) + 8 * half;
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) {
+        v4u x = *(const v4u*)(src + 16 * s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] ^= sign;
+        q[g][s] = __builtin_bit_cast(bf8, x);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kSets; ++g)
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+v"(q[g][s]));
+    // of the wave: keys that all of its queries see, and that any does
+    const int lo = a.causal ? cut(nk - nq + wq + 1, nk) : nk;
+    const int hi = a.causal ? cut(nk - nq + wq + 32 * kSets, nk) : nk;
+
+    f16 o[kSets][kBlocks];
+    float m[kSets], sum[kSets], rsum[kSets];
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) o[g][b] = f16{};
+      m[g] = -INFINITY;
+      sum[g] = rsum[g] = 0.0f;
+    }
+
+    // the lane's chunk of keys mine and mine + 32 of every tile
+    const int mine = 8 * wave + (lane >> 3), place = (lane & 7) ^ swizzle(mine);
+    const char* kv = (const char*)a.kv + ((size_t)k0 * a.heads + h) * (2 * (DN + DV)) + 16 * place;
+    const char* kr = (const char*)a.krope + (size_t)k0 * a.rope_stride * 2 + 16 * (P == 64 ? place : place & 3);
+    const size_t kv_row = (size_t)a.heads * (2 * (DN + DV)), kr_row = (size_t)a.rope_stride * 2;
+    auto load = [&](int t) {
+      const uint32_t to = lds0 + (t & 1) * S::kTileBytes + 1024 * wave;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = t * kKeys + 32 * i + mine;
+        const char* p = j < nk ? kv + j * kv_row : (const char*)zero_key + 16 * place;
+        const char* r = j < nk ? kr + j * kr_row : (const char*)zero_key;
+        load_part<0, S::kColBytes>(p, to + 4096 * i, std::make_integer_sequence<int, DN / 64>());
+        load_to_lds<0>(r, to + 4096 * i + DN / 64 * S::kColBytes);
+        load_part<2 * DN, S::kColBytes>(p, to + 4096 * i + S::kKeyCols * S::kColBytes,
+                                        std::make_integer_sequence<int, DV / 64>());
+      }
+    };
+    if (t0 < t1) load(t0);
+    for (int t = t0; t < t1; ++t) {
+      wait_loads_and_meet<0>();
+      if (t + 1 < t1) load(t + 1);  // into the tile that every wave has left
+      const char* tile = smem + (t & 1) * S::kTileBytes;
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const int key = t * kKeys + 32 * blk;
+        if (key >= hi) break;
+        f16 s0[kSets];
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) s0[g] = f16{};
+#pragma unroll
+        for (int s = 0; s < S::kSteps; ++s) {
+          const bf8 k = *(const bf8*)(tile + kat[s & 3] + S::kColBytes * (s >> 2) + 4096 * blk);
+#pragma unroll
+          for (int g = 0; g < kSets; ++g) s0[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[g][s], s0[g], 0, 0, 0);
+        }
+        bf8 p[kSets][2];
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+          if (key + 32 > lo) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              s0[g][i] = key + 8 * (i / 4) + i % 4 + 4 * half < limit[g] ? s0[g][i] : -INFINITY;
+          }
+          float top = s0[g][0];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) top = fmaxf(top, s0[g][i]);
+          top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+          if (__any(top > m[g] + kSlack)) {
+            const float to = fmaxf(m[g], top);
+            const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
+            m[g] = to;
+            sum[g] *= c;
+            rsum[g] *= c;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) rescale(o[g][b], c);
+          }
+          const float m0 = m[g] == -INFINITY ? 0.0f : m[g];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float w = __builtin_amdgcn_exp2f(fmaf(s0[g][i], scale, -m0));
+            const __bf16 r = (__bf16)w;
+            sum[g] += w;
+            rsum[g] += (float)r;
+            p[g][i / 8][i % 8] = r;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bf8 v = read_across(tile + vat[b & 1] + S::kColBytes * (b >> 1) + 4096 * blk + 2048 * j);
+#pragma unroll
+            for (int g = 0; g < kSets; ++g) o[g][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[g][j], o[g][b], 0, 0, 0);
+          }
+      }
+    }
+    asm volatile("s_barrier" ::: "memory");  // every wave has left the tiles
+
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+      sum[g] += __shfl_xor(sum[g], 32);
+      rsum[g] += __shfl_xor(rsum[g], 32);
+      const int i = wq + 32 * g + col;
+      if (i >= nq) continue;
+      const size_t qh = (size_t)(q0 + i) * a.heads + h;
+      if (a.splits == 1) {
+        const float f = rsum[g] > 0.0f ? 1.0f / rsum[g] : rsum[g] == 0.0f ? 0.0f : rsum[g];
+        __bf16* dst = (__bf16*)a.o + qh * DV + 4 * half;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            bf4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = (__bf16)(o[g][b][4 * c + j] * f);
+            *(bf4*)(dst + 32 * b + 8 * c) = v;
+          }
+        if (a.lse && half == 0)
+          a.lse[qh] = sum[g] > 0.0f ? m[g] * kLn2 + logf(sum[g]) : sum[g] == 0.0f ? -INFINITY : sum[g];
+        continue;
+      }
+      // partial results: (m, sum, rsum, -) and the values of every query, head and part
+      const size_t ph = qh * a.splits + split;
+      if (half == 0) *(f4*)(a.work + ph * 4) = f4{m[g], sum[g], rsum[g], 0.0f};
+      float* dst = a.work + (size_t)a.n_q * a.heads * a.splits * 4 + ph * DV + 4 * half;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *(f4*)(dst + 32 * b + 8 * c) = f4{o[g][b][4 * c], o[g][b][4 * c + 1], o[g][b][4 * c + 2], o[g][b][4 * c + 3]};
+    }
+  }
+}
+
+// Joins the parts of each query and head in their order: one wave for both, DV / 64 values a lane.
+template <int DV>
+__global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
+  constexpr int kPer = DV / 64;
+  const int lane = threadIdx.x & 63;
+  // rows behind the last sequence have no parts
+  const size_t n = (size_t)cut(a.cu_q[a.R], a.n_q) * a.heads;
+  for (size_t qh = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6); qh < n; qh += (size_t)gridDim.x * 4) {
+    const f4* st = (const f4*)a.work + qh * a.splits;
+    float m = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, st[s][0]);
+    const float m0 = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f, rsum = 0.0f, o[kPer] = {};
+    const float* src = a.work + (size_t)a.n_q * a.heads * a.splits * 4 + qh * a.splits * DV + lane * kPer;
+    for (int s = 0; s < a.splits; ++s) {
+      const f4 v = st[s];
+      const float c = __builtin_amdgcn_exp2f(v[0] - m0);
+      sum += c * v[1];
+      rsum += c * v[2];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] += c * src[(size_t)s * DV + i];
+    }
+    const float f = rsum > 0.0f ? 1.0f / rsum : rsum == 0.0f ? 0.0f : rsum;
+    __bf16* dst = (__bf16*)a.o + qh * DV + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) dst[i] = (__bf16)(o[i] * f);
+    if (a.lse && lane == 0) a.lse[qh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
+  }
+}
+
+constexpr int sets_of(int value) { return value == 256 ? 1 : 2; }
+
+template <int DN, int P, int DV>
+hipError_t launch(const PromptArgs& a, hipStream_t s) {
+  constexpr int kSets = sets_of(DV);
+  using S = PromptShape<DN, P, DV, kSets>;
+  constexpr uint32_t lds = S::kLds;
+  // every sequence but one may leave a tile part empty
+  const int64_t slots = ((int64_t)a.n_q + S::kQueries - 1) / S::kQueries + a.R - 1;
+  hipLaunchKernelGGL((prompt_kernel<DN, P, DV, kSets>), dim3(a.heads * a.splits, (int)(slots < 65535 ? slots : 65535)),
+                     dim3(kPromptThreads), lds, s, a, (int)slots);
+  if (a.splits > 1) {
+    const uint64_t blocks = ((uint64_t)a.n_q * a.heads + 3) / 4;
+    hipLaunchKernelGGL(join_prompt_kernel<DV>, dim3((int)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+template <int DN, int P, int DV>
+hipError_t set_lds() {
+  return hipFuncSetAttribute((const void*)prompt_kernel<DN, P, DV, sets_of(DV)>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)PromptShape<DN, P, DV, sets_of(DV)>::kLds);
 }
 
 }  // namespace
 
+int prompt_splits(int R, int n_q, int n_k, int heads, int value) {
+  const int queries = 128 * sets_of(value);
+  const int64_t groups = ((int64_t)n_q + queries - 1) / queries * heads;
+  if (groups <= 0) return 1;
+  int64_t s = 256 / groups;
+  const int64_t most = n_k / R / 512;
+  if (s > most) s = most;
+  if (s > 16) s = 16;
+  return s < 1 ? 1 : (int)s;
+}
+
+uint64_t prompt_work_bytes(int R, int n_q, int n_k, int heads, int value) {
+  const uint64_t s = (uint64_t)prompt_splits(R, n_q, n_k, heads, value);
+  return s == 1 ? 0 : (uint64_t)n_q * heads * s * (16 + 4ull * value);
+}
+
+hipError_t set_prompt_lds() {
+  for (const auto f : {set_lds<64, 32, 64>, set_lds<64, 64, 64>, set_lds<128, 32, 128>, set_lds<128, 64, 128>,
+                       set_lds<192, 32, 256>, set_lds<192, 64, 256>}) {
+    const hipError_t e = f();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t s) {
   if (a.n_q <= 0) return hipSuccess;
-  hipLaunchKernelGGL(prompt_kernel, dim3(a.n_q < 65536 ? a.n_q : 65536, a.heads), dim3(kPromptThreads), 0, s, a);
-  return hipGetLastError();
+  const bool more = a.rope == 64;
+  if (a.value == 64) return more ? launch<64, 64, 64>(a, s) : launch<64, 32, 64>(a, s);
+  if (a.value == 128) return more ? launch<128, 64, 128>(a, s) : launch<128, 32, 128>(a, s);
+  return more ? launch<192, 64, 256>(a, s) : launch<192, 32, 256>(a, s);
 }
 
 }  // namespace hs

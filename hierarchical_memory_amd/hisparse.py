@@ -27,7 +27,8 @@ HS_ROPE_PAIRS, HS_ROPE_HALVES = 0, 1
 EXPORTED = ("hs_required_sizes", "hs_create", "hs_host_pool", "hs_bind_device", "hs_reset", "hs_resolve",
             "hs_plan", "hs_copy", "hs_trial", "hs_commit", "hs_offload", "hs_advance_tail", "hs_gather",
             "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state", "hs_row_bytes", "hs_map_tokens",
-            "hs_store_rows", "hs_attend_work_bytes", "hs_attend", "hs_attend_prompt", "hs_destroy", "hs_last_error")
+            "hs_store_rows", "hs_attend_work_bytes", "hs_attend", "hs_attend_prompt_work_bytes",
+            "hs_attend_prompt", "hs_destroy", "hs_last_error")
 HS_STATIC_PLAN_BYTES = 8 << 20
 
 
@@ -103,7 +104,9 @@ def lib():
         L.hs_store_rows.argtypes = [vp, fmt, vp, i64, vp, f32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
         L.hs_attend_work_bytes.argtypes = [ctypes.POINTER(HsConfig), fmt, i32, ctypes.POINTER(ctypes.c_uint64)]
         L.hs_attend.argtypes = [vp, fmt, vp, i32, f32, vp, vp, vp, vp, vp, ctypes.c_uint64, vp]
-        L.hs_attend_prompt.argtypes = [vp, vp, vp, vp, i64, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp]
+        L.hs_attend_prompt.argtypes = [vp, vp, vp, vp, i64, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp,
+                                       ctypes.c_uint64, vp]
+        L.hs_attend_prompt_work_bytes.argtypes = [i32] * 7 + [ctypes.POINTER(ctypes.c_uint64)]
         L.hs_destroy.argtypes = [vp]
         L.hs_destroy.restype = None
         L.hs_last_error.argtypes = []
@@ -111,7 +114,8 @@ def lib():
         for name in ("hs_required_sizes", "hs_create", "hs_host_pool", "hs_bind_device", "hs_reset", "hs_resolve",
                      "hs_plan", "hs_copy", "hs_trial", "hs_commit", "hs_offload", "hs_advance_tail", "hs_gather",
                      "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state", "hs_row_bytes",
-                     "hs_map_tokens", "hs_store_rows", "hs_attend_work_bytes", "hs_attend", "hs_attend_prompt"):
+                     "hs_map_tokens", "hs_store_rows", "hs_attend_work_bytes", "hs_attend",
+                     "hs_attend_prompt_work_bytes", "hs_attend_prompt"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -253,6 +257,14 @@ def _stream(stream) -> Optional[int]:
         import torch
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _torch_stream(stream):
+    """The torch stream of a stream argument (torch stream or address), None for the current one."""
+    if stream is None or not isinstance(stream, int):
+        return stream
+    import torch
+    return torch.cuda.ExternalStream(stream)
 
 
 def _ptrs(*tensors):
@@ -457,10 +469,19 @@ def hs_attend(ctx, fmt: HsRowFormat, q, scale: float, out, o, lse=None, gather=N
     _check(lib().hs_attend(ctx, ctypes.byref(fmt), a[0], heads, scale, *a[1:], _bytes(work), _stream(stream)))
 
 
-def hs_attend_prompt(ctx, q, kv, rope, cu_q, cu_k, scale: float, o, lse=None, causal: bool = True, stream=None) -> None:
+def hs_attend_prompt_work_bytes(num_requests: int, n_q: int, n_k: int, heads: int, nope: int, rope: int,
+                                value: int) -> int:
+    n = ctypes.c_uint64()
+    _check(lib().hs_attend_prompt_work_bytes(num_requests, n_q, n_k, heads, nope, rope, value, ctypes.byref(n)))
+    return n.value
+
+
+def hs_attend_prompt(ctx, q, kv, rope, cu_q, cu_k, scale: float, o, lse=None, causal: bool = True, work=None,
+                     stream=None) -> None:
     """q: device bf16 [n_q, heads, nope + rope]; kv: bf16 [n_k, heads, nope + value]; rope: bf16 [n_k, rope], rows of
     any stride that is a multiple of 8 (the rope columns of the latent rows); cu_q, cu_k: int32 [R + 1];
-    o: bf16 [n_q, heads, value]; lse: float32 [n_q, heads] or None."""
+    o: bf16 [n_q, heads, value]; lse: float32 [n_q, heads] or None; work: a device buffer of hs_attend_prompt_work_bytes,
+    or None: one is taken from torch's allocator for the call where it takes one (on the call's stream)."""
     import torch
     lim = _lim(ctx)
     R = lim.R if lim is not None else 0
@@ -480,10 +501,16 @@ def hs_attend_prompt(ctx, q, kv, rope, cu_q, cu_k, scale: float, o, lse=None, ca
     _typed("lse", lse, torch.float32, (n_q, heads), nullable=True)
     if not rope.is_cuda:
         raise ValueError(f"expected a GPU tensor, got one on {rope.device}")
-    _on_device(q, kv, rope, cu_q, cu_k, o, lse)
-    pq, pkv, pcq, pck, po, pl = _ptrs(q, kv, _arg("cu_q", cu_q, lim, R + 1), _arg("cu_k", cu_k, lim, R + 1), o, lse)
+    _on_device(q, kv, rope, cu_q, cu_k, o, lse, work)
+    if work is None and lim is not None:
+        n = hs_attend_prompt_work_bytes(R, n_q, n_k, heads, nope, dr, value)
+        if n:
+            with torch.cuda.stream(_torch_stream(stream)):
+                work = torch.empty((n,), dtype=torch.uint8, device=q.device)
+    pq, pkv, pcq, pck, po, pl, pw = _ptrs(q, kv, _arg("cu_q", cu_q, lim, R + 1), _arg("cu_k", cu_k, lim, R + 1), o, lse,
+                                          work)
     _check(lib().hs_attend_prompt(ctx, pq, pkv, rope.data_ptr(), rope.stride(0) if n_k > 1 else dr, pcq, pck, n_q, n_k,
-                                  heads, nope, dr, value, scale, int(causal), po, pl, _stream(stream)))
+                                  heads, nope, dr, value, scale, int(causal), po, pl, pw, _bytes(work), _stream(stream)))
 
 
 def hs_rebuild_order(ctx, stream=None) -> None:

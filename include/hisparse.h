@@ -427,12 +427,17 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
  *           m tokens); 0: all n
  *   d_o     [n_q][heads][value] bf16, 16-byte aligned;  d_lse [n_q][heads] float32 or NULL. Zeros and -inf for a query
  *           that sees no key. Rows behind the last request are left as they were.
+ *   d_work  hs_attend_prompt_work_bytes bytes of device memory, as in hs_attend (few queries over many keys are shared out
+ *           over the keys too, and joined)
  * heads: 1 .. 512; (nope, value) one of (64, 64), (128, 128), (192, 256); rope 32 or 64; n_q, n_k from 0 to 2^30.
  * Precision as in hs_attend.
  */
+int hs_attend_prompt_work_bytes(int32_t num_requests, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope, int32_t rope,
+                                int32_t value, uint64_t* bytes);
 int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void* d_rope, int64_t rope_stride,
                      const int32_t* d_cu_q, const int32_t* d_cu_k, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope,
-                     int32_t rope, int32_t value, float scale, int32_t causal, void* d_o, float* d_lse, void* stream);
+                     int32_t rope, int32_t value, float scale, int32_t causal, void* d_o, float* d_lse, void* d_work,
+                     uint64_t work_bytes, void* stream);
 
 /* Free the host pool and the context (device buffers belong to the caller). NULL is ignored. */
 void hs_destroy(hs_ctx* ctx);

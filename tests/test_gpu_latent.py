@@ -544,6 +544,35 @@ def test_prompt_long(heads):
     sw.close()
 
 
+@pytest.mark.parametrize("nope,rope,value", DIMS)
+@pytest.mark.parametrize("nq,nk,heads,causal", [([1], [5000], 1, True), ([40, 3, 0], [2600, 1400, 900], 2, True),
+                                                ([7, 90], [4000, 10], 1, False), ([130], [3333], 4, True)])
+def test_prompt_keys_in_parts(nq, nk, heads, causal, nope, rope, value):
+    """Few queries over many keys: each tile's keys are cut into parts and joined, some of them without a key."""
+    pad = 2
+    assert hm.hs_attend_prompt_work_bytes(len(nq), sum(nq) + pad, sum(nk) + pad, heads, nope, rope, value) > 0
+    sw, args = _prompt_case(nq, nk, heads, nope, rope, value, causal, seed=sum(nk), pad=pad)
+    o, lse = args[6].clone(), args[7].clone()
+    n = hm.hs_attend_prompt_work_bytes(len(nq), args[0].shape[0], args[1].shape[0], heads, nope, rope, value)
+    work = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        args[6].fill_(9)
+        torch.cuda.synchronize()
+        hm.hs_attend_prompt(sw.ctx, *args, work=work, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(args[6], o) and torch.equal(args[7], lse)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):  # the work buffer is taken on the call's stream
+        args[6].fill_(9)
+        torch.cuda.synchronize()
+        hm.hs_attend_prompt(sw.ctx, *args, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(args[6], o)
+    with pytest.raises(hm.HiSparseError, match="work buffer"):
+        hm.hs_attend_prompt(sw.ctx, *args, work=work[:n - 16])
+    sw.close()
+
+
 def test_prompt_many_sequences():
     n = [(7 * i) % 23 for i in range(700)]
     sw, _ = _prompt_case(n, [m + i % 3 for i, m in enumerate(n)], 2, 64, 32, 64, True, seed=5)

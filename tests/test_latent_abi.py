@@ -44,6 +44,19 @@ def test_work_bytes():
     assert hm.lib().hs_attend_work_bytes(None, None, 1, None) == hm.HS_E_INVALID
 
 
+def test_prompt_work_bytes():
+    for R, n_q, n_k, heads, dims in ((1, 0, 0, 1, (64, 32, 64)), (4, 512, 16384, 8, (192, 64, 256)),
+                                     (8, 8192, 8192, 16, (128, 64, 128)), (1, 1, 1 << 30, 1, (128, 64, 128))):
+        n = hm.hs_attend_prompt_work_bytes(R, n_q, n_k, heads, *dims)
+        assert n >= 0 and n % 16 == 0
+    for bad, msg in (((0, 1, 1, 1, 128, 64, 128), "num_requests"), ((1, -1, 1, 1, 128, 64, 128), "n_q"),
+                     ((1, 1, -1, 1, 128, 64, 128), "n_k"), ((1, (1 << 30) + 1, 1, 1, 128, 64, 128), "n_q"),
+                     ((1, 1, 1, 0, 128, 64, 128), "heads"), ((1, 1, 1, 1, 128, 48, 128), "rope"),
+                     ((1, 1, 1, 1, 128, 64, 64), "nope, value")):
+        with pytest.raises(hm.HiSparseError, match=msg):
+            hm.hs_attend_prompt_work_bytes(*bad)
+
+
 def test_null_contexts():
     lib = hm.lib()
     assert lib.hs_row_bytes(None, None) == hm.HS_E_INVALID
@@ -52,7 +65,7 @@ def test_null_contexts():
                              None) == hm.HS_E_INVALID
     assert lib.hs_attend(None, None, None, 1, 1.0, None, None, None, None, None, 0, None) == hm.HS_E_INVALID
     assert lib.hs_attend_prompt(None, None, None, None, 0, None, None, 0, 0, 1, 128, 64, 128, 1.0, 1, None, None,
-                                None) == hm.HS_E_INVALID
+                                None, 0, None) == hm.HS_E_INVALID
     assert "NULL" in hm.hs_last_error()
 
 
