@@ -133,20 +133,18 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
 
   // the queries, one k-step of 16 values to a register quadruple
   bf8 q[S::kSteps];
+  const uint32_t sign = a.scale < 0.0f ? kSigns : 0u;
   {
     const int h = head < a.heads ? head : a.heads - 1;  // columns behind the last head repeat it, and are dropped
     const __bf16* src = (const __bf16*)a.q + ((size_t)part.r * a.heads + h) * S::D + 8 * half;
 #pragma unroll
-    for (int s = 0; s < S::kSteps; ++s) q[s] = *(const bf8*)(src + 16 * s);
-    // they are here before any load to LDS is on its way: a wait for them later would be one for those too
-#pragma unroll
-    for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+v"(q[s]));
+    for (int s = 0; s < S::kSteps; ++s) q[s] = turned(*(const v4u*)(src + 16 * s), sign);
   }
   f16 o[kBlocks];
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) o[b] = f16{};
   float m = -INFINITY, sum = 0.0f, rsum = 0.0f;  // rsum: of the weights as rounded for the second product
-  const float scale = a.scale * kLog2e;
+  const float scale = scale_of(a.scale);
 
   // LDS places of this lane's reads, but for the tile's start
   int kat[4], vat[2];
@@ -188,6 +186,9 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
     return (uint32_t)__ballot(rows[col] >= 0);
   };
   write_list(0);
+  // the queries are here before any load to LDS is on its way: a wait for them later would be one for those too
+#pragma unroll
+  for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+v"(q[s]));
   __syncthreads();
   uint32_t there[S::kAhead + 1];  // of the tiles asked for, the one in use first
 #pragma unroll
@@ -225,48 +226,48 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
           s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[(s / kSet) & 1][i], q[s + i], s0, 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    float sc[16];
+    // the values' first blocks are on their way during the softmax, the others two blocks ahead of their product
+    constexpr int kReads = 3;
+    bf8 v[kReads][2];
+    auto read_values = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sc[i] = s0[i] * scale;
+      for (int j = 0; j < 2; ++j) v[b % kReads][j] = read_across(tile + vat[b & 1] + S::kColBytes * (b >> 1) + 2048 * j);
+    };
+    read_values(0);
+    read_values(1);
     if (there[0] != 0xffffffffu) {
       const uint32_t mask = there[0] >> (4 * half);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sc[i] = (mask >> (8 * (i / 4) + i % 4)) & 1 ? sc[i] : -INFINITY;
+      for (int i = 0; i < 16; ++i) s0[i] = (mask >> (8 * (i / 4) + i % 4)) & 1 ? s0[i] : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < S::kAhead; ++i) there[i] = there[i + 1];
-    float top = sc[0];
+    float top = s0[0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, sc[i]);
-    top = fmaxf(top, __shfl_xor(top, 32));
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s0[i]);
+    top = fmaxf(top, __shfl_xor(top, 32)) * scale;
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top);
-      const float c = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - to);
-      m = to;
-      sum *= c;
-      rsum *= c;
+      if (__any(m > -INFINITY)) {
+        const float c = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - to);
+        sum *= c;
+        rsum *= c;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) rescale(o[b], c);
+        for (int b = 0; b < kBlocks; ++b) rescale(o[b], c);
+      }
+      m = to;
     }
     const float m0 = m == -INFINITY ? 0.0f : m;
     bf8 p[2];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float w = __builtin_amdgcn_exp2f(sc[i] - m0);
-      const __bf16 r = (__bf16)w;
-      sum += w;
-      rsum += (float)r;
-      p[i / 8][i % 8] = r;
-    }
+    weights(s0, scale, m0, p, sum, rsum);
+    __builtin_amdgcn_sched_barrier(0);
     // O^T
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
+      if (b + 2 < kBlocks) read_values(b + 2);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bf8 v = read_across(tile + vat[b & 1] + S::kColBytes * (b >> 1) + 2048 * j);
-        o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[j], o[b], 0, 0, 0);
-      }
-      if (b & 1) __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < 2; ++j) o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[b % kReads][j], p[j], o[b], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads behind the last tile write to LDS too

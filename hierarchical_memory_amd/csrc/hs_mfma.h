@@ -1,8 +1,7 @@
 // What the two attention kernels share: types, loads past the registers into LDS, LDS places, accumulators (gfx950).
 #pragma once
 
-#include <hip/hip_runtime.h>
-#include <stdint.h>
+#include "hs_internal.h"
 
 namespace hs {
 
@@ -42,8 +41,21 @@ __device__ __forceinline__ void load_to_lds(const char* p, uint32_t lds) {
 // one group.
 __device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
+// A query's eight values, their signs turned where the scale is negative: scores are then scaled by its magnitude, which
+// keeps their order.
+constexpr uint32_t kSigns = 0x80008000u;
+__device__ __forceinline__ bf8 turned(v4u x, uint32_t sign) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] ^= sign;
+  return __builtin_bit_cast(bf8, x);
+}
+
+// The magnitude of the scale, to base 2. Not zero: a score that a mask took out, -infinity, stays so.
+__device__ __forceinline__ float scale_of(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1.17549435e-38f); }
+
 // The accumulators stay in the matrix unit's half of the registers, which other instructions do not reach: one at a time
-// out, multiplied, and back. Seldom run.
+// out, multiplied, and back. Seldom run. (The waits are those between the matrix unit's and other instructions, which the
+// compiler does not see inside an asm block.)
 __device__ __forceinline__ void rescale(f16& o, float c) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -52,6 +64,22 @@ __device__ __forceinline__ void rescale(f16& o, float c) {
         : "+a"(x), "=&v"(y)
         : "v"(c));
     o[i] = x;
+  }
+}
+
+// The weights 2^(s scale - m) of a lane's 16 scores, rounded to bf16 in p for the second product; their sum is added to
+// `sum`, that of the rounded ones to `rsum`. Two rounded weights are summed by one dot product with ones.
+__device__ __forceinline__ void weights(const f16& s, float scale, float m, bf8 p[2], float& sum, float& rsum) {
+  const bf2 ones = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float a = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m)), b = __builtin_amdgcn_exp2f(fmaf(s[i + 1], scale, -m));
+    const bf2 r = {(__bf16)a, (__bf16)b};
+    sum += a;
+    sum += b;
+    rsum = __builtin_amdgcn_fdot2_f32_bf16(r, ones, rsum, false);
+    p[i / 8][i % 8] = r[0];
+    p[i / 8][i % 8 + 1] = r[1];
   }
 }
 

@@ -101,8 +101,8 @@ __global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a,
   for (int i = 0; i < 4; ++i) kat[i] = col * 128 + (((2 * i + half) ^ swizzle(col)) << 4);
 #pragma unroll
   for (int i = 0; i < 2; ++i) vat[i] = across_place(lane, i) + S::kKeyCols * S::kColBytes;
-  const float scale = fabsf(a.scale) * kLog2e;
-  const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale turns the queries round
+  const float scale = scale_of(a.scale);
+  const uint32_t sign = a.scale < 0.0f ? kSigns : 0u;
 
   for (int slot = blockIdx.y; slot < slots; slot += gridDim.y) {
     // the last tiles of a sequence see the most keys, and go first
@@ -129,10 +129,7 @@ __global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a,
       const __bf16* src = (const __bf16*)a.q + ((size_t)(q0 + j) * a.heads + h) * (DN + P) + 8 * half;
 #pragma unroll
       for (int s = 0; s < S::kSteps; ++s) {
-        v4u x = *(const v4u*)(src + 16 * s);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] ^= sign;
-        q[g][s] = __builtin_bit_cast(bf8, x);
+        q[g][s] = turned(*(const v4u*)(src + 16 * s), sign);
       }
     }
 #pragma unroll
@@ -203,22 +200,16 @@ __global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a,
           top = fmaxf(top, __shfl_xor(top, 32)) * scale;
           if (__any(top > m[g] + kSlack)) {
             const float to = fmaxf(m[g], top);
-            const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
+            if (__any(m[g] > -INFINITY)) {
+              const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
+              sum[g] *= c;
+              rsum[g] *= c;
+#pragma unroll
+              for (int b = 0; b < kBlocks; ++b) rescale(o[g][b], c);
+            }
             m[g] = to;
-            sum[g] *= c;
-            rsum[g] *= c;
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) rescale(o[g][b], c);
           }
-          const float m0 = m[g] == -INFINITY ? 0.0f : m[g];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float w = __builtin_amdgcn_exp2f(fmaf(s0[g][i], scale, -m0));
-            const __bf16 r = (__bf16)w;
-            sum[g] += w;
-            rsum[g] += (float)r;
-            p[g][i / 8][i % 8] = r;
-          }
+          weights(s0[g], scale, m[g] == -INFINITY ? 0.0f : m[g], p[g], sum[g], rsum[g]);
         }
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)

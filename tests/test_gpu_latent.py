@@ -490,7 +490,7 @@ def _cu(n):
     return torch.tensor([0] + list(n), dtype=torch.int64).cumsum(0).to(torch.int32)
 
 
-def _prompt_case(nq, nk, heads, nope, rope, value, causal, seed=0, pad=3, qstd=1.0, latent=256, check=True):
+def _prompt_case(nq, nk, heads, nope, rope, value, causal, seed=0, pad=3, qstd=1.0, latent=256, check=True, scale=None):
     gen = torch.Generator().manual_seed(seed)
     R, N, M = len(nq), sum(nq) + pad, sum(nk) + pad
     sw = hm.SwapIn(hm.config(R, 1, 1, 0.0, 16, 4, 0))
@@ -500,7 +500,7 @@ def _prompt_case(nq, nk, heads, nope, rope, value, causal, seed=0, pad=3, qstd=1
     kv[sum(nk):], rows[sum(nk):] = float("nan"), float("nan")  # keys behind the last sequence
     o = torch.full((N, heads, value), 9.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((N, heads), 9.0, device="cuda")
-    scale = (nope + rope) ** -0.5
+    scale = (nope + rope) ** -0.5 if scale is None else scale
     cu_q, cu_k = _cu(nq), _cu(nk)
     args = (q.cuda(), kv.cuda(), rows.cuda()[:, latent:], cu_q.cuda(), cu_k.cuda(), scale, o, lse, causal)
     hm.hs_attend_prompt(sw.ctx, *args)
@@ -535,6 +535,14 @@ PROMPTS = [  # (queries, keys, heads)
 @pytest.mark.parametrize("nq,nk,heads", PROMPTS, ids=range(len(PROMPTS)))
 def test_prompt(nq, nk, heads, nope, rope, value, causal):
     sw, _ = _prompt_case(nq, nk, heads, nope, rope, value, causal, seed=len(nq) + nope)
+    sw.close()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_prompt_scales(scale, causal):
+    """Uniform weights, reversed scores, and scores so far apart that most weights vanish and the maximum moves."""
+    sw, _ = _prompt_case([150, 70], [150, 300], 2, 128, 64, 128, causal, seed=11, scale=scale)
     sw.close()
 
 
