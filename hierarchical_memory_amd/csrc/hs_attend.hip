@@ -147,11 +147,11 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
   const float scale = scale_of(a.scale);
 
   // LDS places of this lane's reads, but for the tile's start
-  int kat[4], vat[2];
+  int kat[4], vat[2][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) kat[i] = col * 128 + (((2 * i + half) ^ swizzle(col)) << 4);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) vat[i] = across_place(lane, i) + S::kColBytes * (kBlocks / 2 * share);
+  for (int i = 0; i < 4; ++i) vat[i / 2][i % 2] = across_place(lane, i / 2, 8 * (i % 2)) + S::kColBytes * (kBlocks / 2 * share);
 
   const int tiles = (part.end - part.begin + kTile - 1) / kTile;
   auto write_list = [&](int from) {  // of the rows [from, from + kListed) of the part
@@ -231,7 +231,10 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
     bf8 v[kReads][2];
     auto read_values = [&](int b) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) v[b % kReads][j] = read_across(tile + vat[b & 1] + S::kColBytes * (b >> 1) + 2048 * j);
+      for (int j = 0; j < 2; ++j) {
+        const char* at = tile + S::kColBytes * (b >> 1) + 2048 * j;
+        v[b % kReads][j] = read_across(at + vat[b & 1][0], at + vat[b & 1][1]);
+      }
     };
     read_values(0);
     read_values(1);

@@ -27,19 +27,19 @@ __device__ __forceinline__ void wait_loads_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// 16 bytes of each lane's address + kOffset to LDS at lds + 16 * lane (the instruction adds its offset to both).
+// 16 bytes of each lane's address + kOffset to LDS at lds + 16 * lane (the instruction adds its offset to both). It takes the LDS
+// address from m0, a register that the compiler sets right before each use of its own and keeps nothing in.
 template <int kOffset>
 __device__ __forceinline__ void load_to_lds(const char* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds - kOffset), "v"(p),
                "n"(kOffset)
-               : "memory", "m0");
+               : "memory");
 }
 
 // A tile in LDS: its rows' columns in groups of 64 values (128 bytes), one group of all rows after another, and the eight
-// 16-byte chunks of a group changing places by the row, so that neither reading eight rows at one chunk nor four rows at a
-// pair of chunks meets a bank twice. A wave's asynchronous load (16 bytes a lane, in order, into LDS) fills eight rows of
-// one group.
-__device__ __forceinline__ int swizzle(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+// 16-byte chunks of a group changing places by the row: 16 rows read at one chunk, and 4 rows at four chunks, meet no bank of
+// the 64 twice. A wave's asynchronous load (16 bytes a lane, in order, into LDS) fills eight rows of one group.
+__device__ __forceinline__ int swizzle(int row) { return ((row >> 1) & 1) << 2 | ((row >> 2) & 3); }
 
 // A query's eight values, their signs turned where the scale is negative: scores are then scaled by its magnitude, which
 // keeps their order.
@@ -83,18 +83,18 @@ __device__ __forceinline__ void weights(const f16& s, float scale, float m, bf8 
   }
 }
 
-// The matrix unit's second operand read across a tile's rows: lane (column d = lane % 32 of the 32 that `at` begins) gets rows
-// 4 half + 0..3 and 8 + 4 half + 0..3 of the 16 that begin there, half = lane / 32.
-__device__ __forceinline__ bf8 read_across(const char* at) {
-  const HS_LDS char* p = (const HS_LDS char*)at;
-  const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)p);
-  const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(p + 1024));
-  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+// The matrix unit's first operand read across a tile's rows: lane (column d = lane % 32 of the 32 that `lo` begins) gets rows
+// 4 half + 0..3 (from lo) and 8 + 4 half + 0..3 (from hi) of the 16 that begin there, half = lane / 32.
+__device__ __forceinline__ bf8 read_across(const char* lo, const char* hi) {
+  const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(const HS_LDS char*)lo);
+  const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(const HS_LDS char*)hi);
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Where read_across starts in a group of columns for this lane: its row and chunk, for the first and second 32 columns.
-__device__ __forceinline__ int across_place(int lane, int second) {
-  const int row = 4 * (lane >> 5) + ((lane & 15) >> 2), x = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+// Where read_across reads in a group of columns for this lane: its row and chunk, for the first and second 32 columns and
+// the rows from 0 and from 8 on.
+__device__ __forceinline__ int across_place(int lane, int second, int from) {
+  const int row = from + 4 * (lane >> 5) + ((lane & 15) >> 2), x = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
   return row * 128 + (((x ^ swizzle(row)) ^ (4 * second)) << 4) + 8 * (lane & 1);
 }
 

@@ -18,8 +18,6 @@ namespace hs {
 
 namespace {
 
-constexpr int kPromptThreads = 256;
-constexpr int kPromptWaves = 4;
 constexpr int kKeys = 64;  // of a tile
 
 __device__ __align__(16) uint4 zero_key[64];  // what a tile holds behind the last key
@@ -27,23 +25,26 @@ __device__ __align__(16) uint4 zero_key[64];  // what a tile holds behind the la
 // DN, P: nope and rope values of a key, DV: of a value. kSets: column sets of 32 queries of a wave.
 template <int DN, int P, int DV, int kSets>
 struct PromptShape {
-  static constexpr int kQueries = 32 * kSets * kPromptWaves;
+  // two waves to a SIMD where a wave's part of the output leaves the registers for it: one's softmax beside the other's products
+  static constexpr int kWaves = DV == 256 ? 4 : 8;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kQueries = 32 * kSets * kWaves;
   static constexpr int kSteps = (DN + P) / 16;
   static constexpr int kKeyCols = DN / 64 + 1, kValueCols = DV / 64;  // groups of 64 columns (the last key group: rope)
   static constexpr int kColBytes = kKeys * 128;
   static constexpr int kTileBytes = (kKeyCols + kValueCols) * kColBytes;
-  static constexpr int kLoads = 2 * (kKeyCols + kValueCols);  // of a lane, for a tile
+  static constexpr int kLoads = 8 / kWaves * (kKeyCols + kValueCols);  // of a lane, for a tile
   static constexpr uint32_t kLds = 2 * kTileBytes;
 };
 
 __device__ __forceinline__ int cut(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
-// The sequence of query tile `id` and the tile's number in it: a scan over the sequences' tile counts, 256 at a time.
-template <int kQueries>
+// The sequence of query tile `id` and the tile's number in it: a scan over the sequences' tile counts, one to a thread.
+template <int kQueries, int kWaves>
 __device__ __forceinline__ bool find_tile(const PromptArgs& a, int id, int* seq, int* tile, int* sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int before = 0;
-  for (int r0 = 0; r0 < a.R; r0 += kPromptThreads) {
+  for (int r0 = 0; r0 < a.R; r0 += 64 * kWaves) {
     const int r = r0 + tid;
     int c = 0;
     if (r < a.R) {
@@ -57,19 +58,19 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int id, int* seq,
       if (lane >= d) x += y;
     }
     if (lane == 63) sh[wave] = x;
-    if (tid == 0) sh[4] = -1;
+    if (tid == 0) sh[kWaves] = -1;
     __syncthreads();
     int total = 0;
-    for (int w = 0; w < kPromptWaves; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       if (w < wave) x += sh[w];
       total += sh[w];
     }
     if (id >= before + x - c && id < before + x) {
-      sh[4] = r;
-      sh[5] = id - (before + x - c);
+      sh[kWaves] = r;
+      sh[kWaves + 1] = id - (before + x - c);
     }
     __syncthreads();
-    const int found = sh[4], at = sh[5];
+    const int found = sh[kWaves], at = sh[kWaves + 1];
     __syncthreads();
     if (found >= 0) {
       *seq = __builtin_amdgcn_readfirstlane(found);
@@ -87,27 +88,28 @@ __device__ __forceinline__ void load_part(const char* row, uint32_t lds, std::in
 }
 
 template <int DN, int P, int DV, int kSets>
-__global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a, int slots) {
+__global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void prompt_kernel(PromptArgs a, int slots) {
   using S = PromptShape<DN, P, DV, kSets>;
+  constexpr int kWaves = S::kWaves;
   constexpr int kBlocks = DV / 32;
   extern __shared__ __align__(1024) char smem[];
-  __shared__ int sh[6];
+  __shared__ int sh[kWaves + 2];
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(HS_LDS char*)smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int h = blockIdx.x % a.heads, split = blockIdx.x / a.heads;
-  int kat[4], vat[2];
+  int kat[4], vat[2][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) kat[i] = col * 128 + (((2 * i + half) ^ swizzle(col)) << 4);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) vat[i] = across_place(lane, i) + S::kKeyCols * S::kColBytes;
+  for (int i = 0; i < 4; ++i) vat[i / 2][i % 2] = across_place(lane, i / 2, 8 * (i % 2)) + S::kKeyCols * S::kColBytes;
   const float scale = scale_of(a.scale);
   const uint32_t sign = a.scale < 0.0f ? kSigns : 0u;
 
   for (int slot = blockIdx.y; slot < slots; slot += gridDim.y) {
     // the last tiles of a sequence see the most keys, and go first
     int seq, qt;
-    if (!find_tile<S::kQueries>(a, slots - 1 - slot, &seq, &qt, sh)) continue;
+    if (!find_tile<S::kQueries, kWaves>(a, slots - 1 - slot, &seq, &qt, sh)) continue;
     const int q0 = cut(a.cu_q[seq], a.n_q), nq = cut(a.cu_q[seq + 1], a.n_q) - q0;
     const int k0 = cut(a.cu_k[seq], a.n_k);
     int nk = cut(a.cu_k[seq + 1], a.n_k) - k0;
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a,
 #pragma unroll
     for (int g = 0; g < kSets; ++g)
 #pragma unroll
-      for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+v"(q[g][s]));
+      for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+a"(q[g][s]));
     // of the wave: keys that all of its queries see, and that any does
     const int lo = a.causal ? cut(nk - nq + wq + 1, nk) : nk;
     const int hi = a.causal ? cut(nk - nq + wq + 32 * kSets, nk) : nk;
@@ -150,22 +152,21 @@ __global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a,
       sum[g] = rsum[g] = 0.0f;
     }
 
-    // the lane's chunk of keys mine and mine + 32 of every tile
+    // the lane's chunk of a key (two keys 32 apart) of every tile
     const int mine = 8 * wave + (lane >> 3), place = (lane & 7) ^ swizzle(mine);
     const char* kv = (const char*)a.kv + ((size_t)k0 * a.heads + h) * (2 * (DN + DV)) + 16 * place;
     const char* kr = (const char*)a.krope + (size_t)k0 * a.rope_stride * 2 + 16 * (P == 64 ? place : place & 3);
     const size_t kv_row = (size_t)a.heads * (2 * (DN + DV)), kr_row = (size_t)a.rope_stride * 2;
     auto load = [&](int t) {
-      const uint32_t to = lds0 + (t & 1) * S::kTileBytes + 1024 * wave;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = t * kKeys + 32 * i + mine;
+      for (int i = 0; i < 8 / kWaves; ++i) {
+        const uint32_t to = lds0 + (t & 1) * S::kTileBytes + 1024 * (wave + i * kWaves);
+        const int j = t * kKeys + 8 * i * kWaves + mine;
         const char* p = j < nk ? kv + j * kv_row : (const char*)zero_key + 16 * place;
         const char* r = j < nk ? kr + j * kr_row : (const char*)zero_key;
-        load_part<0, S::kColBytes>(p, to + 4096 * i, std::make_integer_sequence<int, DN / 64>());
-        load_to_lds<0>(r, to + 4096 * i + DN / 64 * S::kColBytes);
-        load_part<2 * DN, S::kColBytes>(p, to + 4096 * i + S::kKeyCols * S::kColBytes,
-                                        std::make_integer_sequence<int, DV / 64>());
+        load_part<0, S::kColBytes>(p, to, std::make_integer_sequence<int, DN / 64>());
+        load_to_lds<0>(r, to + DN / 64 * S::kColBytes);
+        load_part<2 * DN, S::kColBytes>(p, to + S::kKeyCols * S::kColBytes, std::make_integer_sequence<int, DV / 64>());
       }
     };
     if (t0 < t1) load(t0);
@@ -180,12 +181,35 @@ __global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a,
         f16 s0[kSets];
 #pragma unroll
         for (int g = 0; g < kSets; ++g) s0[g] = f16{};
+        constexpr int kSet = 4;  // k-steps whose keys are read before the steps before them are multiplied
+        bf8 k[2][kSet];
 #pragma unroll
-        for (int s = 0; s < S::kSteps; ++s) {
-          const bf8 k = *(const bf8*)(tile + kat[s & 3] + S::kColBytes * (s >> 2) + 4096 * blk);
+        for (int i = 0; i < kSet; ++i) k[0][i] = *(const bf8*)(tile + kat[i] + 4096 * blk);
 #pragma unroll
-          for (int g = 0; g < kSets; ++g) s0[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[g][s], s0[g], 0, 0, 0);
+        for (int s = 0; s < S::kSteps; s += kSet) {
+#pragma unroll
+          for (int i = 0; i < kSet; ++i)
+            if (s + kSet + i < S::kSteps)
+              k[(s / kSet + 1) & 1][i] = *(const bf8*)(tile + kat[i] + S::kColBytes * ((s + kSet + i) >> 2) + 4096 * blk);
+#pragma unroll
+          for (int i = 0; i < kSet; ++i)
+            if (s + i < S::kSteps)
+#pragma unroll
+              for (int g = 0; g < kSets; ++g)
+                s0[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[(s / kSet) & 1][i], q[g][s + i], s0[g], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
+        constexpr int kReads = 2;
+        bf8 v[kReads][2];
+        auto read_values = [&](int b) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const char* at = tile + S::kColBytes * (b >> 1) + 4096 * blk + 2048 * j;
+            v[b % kReads][j] = read_across(at + vat[b & 1][0], at + vat[b & 1][1]);
+          }
+        };
+#pragma unroll
+        for (int b = 0; b < kReads - 1; ++b) read_values(b);
         bf8 p[kSets][2];
 #pragma unroll
         for (int g = 0; g < kSets; ++g) {
@@ -211,14 +235,17 @@ __global__ __launch_bounds__(kPromptThreads, 1) void prompt_kernel(PromptArgs a,
           }
           weights(s0[g], scale, m[g] == -INFINITY ? 0.0f : m[g], p[g], sum[g], rsum[g]);
         }
+        // O^T, the values read kReads - 1 blocks ahead of their product
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+        for (int b = 0; b < kBlocks; ++b) {
+          if (b + kReads - 1 < kBlocks) read_values(b + kReads - 1);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const bf8 v = read_across(tile + vat[b & 1] + S::kColBytes * (b >> 1) + 4096 * blk + 2048 * j);
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int g = 0; g < kSets; ++g) o[g][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[g][j], o[g][b], 0, 0, 0);
-          }
+            for (int g = 0; g < kSets; ++g)
+              o[g][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[b % kReads][j], p[g][j], o[g][b], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     asm volatile("s_barrier" ::: "memory");  // every wave has left the tiles
@@ -289,7 +316,7 @@ __global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
   }
 }
 
-constexpr int sets_of(int value) { return value == 256 ? 1 : 2; }
+constexpr int sets_of(int) { return 1; }
 
 template <int DN, int P, int DV>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
@@ -299,7 +326,7 @@ hipError_t launch(const PromptArgs& a, hipStream_t s) {
   // every sequence but one may leave a tile part empty
   const int64_t slots = ((int64_t)a.n_q + S::kQueries - 1) / S::kQueries + a.R - 1;
   hipLaunchKernelGGL((prompt_kernel<DN, P, DV, kSets>), dim3(a.heads * a.splits, (int)(slots < 65535 ? slots : 65535)),
-                     dim3(kPromptThreads), lds, s, a, (int)slots);
+                     dim3(S::kThreads), lds, s, a, (int)slots);
   if (a.splits > 1) {
     const uint64_t blocks = ((uint64_t)a.n_q * a.heads + 3) / 4;
     hipLaunchKernelGGL(join_prompt_kernel<DV>, dim3((int)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
@@ -316,7 +343,7 @@ hipError_t set_lds() {
 }  // namespace
 
 int prompt_splits(int R, int n_q, int n_k, int heads, int value) {
-  const int queries = 128 * sets_of(value);
+  const int queries = value == 256 ? 128 : 256;
   const int64_t groups = ((int64_t)n_q + queries - 1) / queries * heads;
   if (groups <= 0) return 1;
   int64_t s = 256 / groups;
