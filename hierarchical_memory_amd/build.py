@@ -24,6 +24,13 @@ FLAGS = [
     "-I", INCLUDE, "-I", CSRC,
 ]
 
+# The attention kernels: matrix instructions whose results other instructions read (scores) write to the ordinary registers
+MFMA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+
+
+def flags_of(src: str):
+    return FLAGS + (MFMA_FLAGS if os.path.basename(src) in ("hs_attend.hip", "hs_prompt.hip") else [])
+
 
 def build(verbose: bool = False) -> str:
     def run(cmd):
@@ -38,7 +45,7 @@ def build(verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory() as objects:
         out = [os.path.join(objects, os.path.basename(src) + ".o") for src in SOURCES]
         with ThreadPoolExecutor(len(SOURCES)) as pool:
-            list(pool.map(lambda so: run([HIPCC, *FLAGS, "-c", so[0], "-o", so[1]]), zip(SOURCES, out)))
+            list(pool.map(lambda so: run([HIPCC, *flags_of(so[0]), "-c", so[0], "-o", so[1]]), zip(SOURCES, out)))
         tmp = LIB + ".tmp"
         run([HIPCC, *FLAGS, "-shared", "-o", tmp, *out])
     os.replace(tmp, LIB)

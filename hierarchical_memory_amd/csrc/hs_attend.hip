@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
         sum *= c;
         rsum *= c;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) rescale(o[b], c);
+        for (int b = 0; b < kBlocks; ++b) o[b] *= c;
       }
       m = to;
     }

@@ -53,20 +53,6 @@ __device__ __forceinline__ bf8 turned(v4u x, uint32_t sign) {
 // The magnitude of the scale, to base 2. Not zero: a score that a mask took out, -infinity, stays so.
 __device__ __forceinline__ float scale_of(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1.17549435e-38f); }
 
-// The accumulators stay in the matrix unit's half of the registers, which other instructions do not reach: one at a time
-// out, multiplied, and back. Seldom run. (The waits are those between the matrix unit's and other instructions, which the
-// compiler does not see inside an asm block.)
-__device__ __forceinline__ void rescale(f16& o, float c) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float x = o[i], y;
-    asm("s_nop 7\n\tv_accvgpr_read_b32 %1, %0\n\ts_nop 1\n\tv_mul_f32 %1, %1, %2\n\ts_nop 1\n\tv_accvgpr_write_b32 %0, %1\n\ts_nop 3"
-        : "+a"(x), "=&v"(y)
-        : "v"(c));
-    o[i] = x;
-  }
-}
-
 // The weights 2^(s scale - m) of a lane's 16 scores, rounded to bf16 in p for the second product; their sum is added to
 // `sum`, that of the rounded ones to `rsum`. Two rounded weights are summed by one dot product with ones.
 __device__ __forceinline__ void weights(const f16& s, float scale, float m, bf8 p[2], float& sum, float& rsum) {

@@ -229,7 +229,7 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
               sum[g] *= c;
               rsum[g] *= c;
 #pragma unroll
-              for (int b = 0; b < kBlocks; ++b) rescale(o[g][b], c);
+              for (int b = 0; b < kBlocks; ++b) o[g][b] *= c;
             }
             m[g] = to;
           }
