@@ -248,7 +248,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
     float top = s0[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s0[i]);
-    top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+    top = max_of_halves(top) * scale;
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top);
       if (__any(m > -INFINITY)) {
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
     }
     const float m0 = m == -INFINITY ? 0.0f : m;
     bf8 p[2];
-    weights(s0, scale, m0, p, sum, rsum);
+    weigh(s0, scale, m0, p, sum, rsum);
     __builtin_amdgcn_sched_barrier(0);
     // O^T
 #pragma unroll

@@ -3,12 +3,14 @@
 //
 //   s = scale * q . key,   o = sum_j p_j value_j / sum_j p_j,   p_j = 2^(s_j log2 e - m)   (m a running maximum)
 //
-// One pass over the keys, 64 to a tile, two tiles in LDS. A workgroup of four waves takes 128 (256) queries of one sequence
-// and head, 32 (64) to a wave. Matrix instructions do both products transposed, so that a query is a lane's column in both
-// and its maximum, sum and rescaling stay inside the lane:
+// One pass over the keys. A workgroup of four waves takes 256 (128) queries of one sequence and head, 64 (32) to a wave.
+// Matrix instructions do both products transposed, so that a query is a lane's column in both and its maximum, sum and
+// rescaling stay inside the lane:
 //   S^T[key][query]  = K Q^T     A: keys from LDS, B: the queries, kept in registers
 //   O^T[dim][query] += V^T P^T   A: values read through the transposing LDS load, B: the weights as S^T left them
 // (a lane half h holds the keys 8 i + 4 h + 0..3 of S^T; the second product takes its keys in that order).
+// There is one wave to a SIMD, so the two pipes are kept busy from within it: a step of 32 keys computes the next step's
+// scores between the exponentials of its own, and takes their maximum between its products with the values.
 #include "hs_latent.h"
 #include "hs_mfma.h"
 
@@ -18,24 +20,34 @@ namespace hs {
 
 namespace {
 
-constexpr int kKeys = 64;  // of a tile
-
 __device__ __align__(16) uint4 zero_key[64];  // what a tile holds behind the last key
 
 // DN, P: nope and rope values of a key, DV: of a value. kSets: column sets of 32 queries of a wave.
 template <int DN, int P, int DV, int kSets>
 struct PromptShape {
-  // two waves to a SIMD where a wave's part of the output leaves the registers for it: one's softmax beside the other's products
-  static constexpr int kWaves = DV == 256 ? 4 : 8;
+  static constexpr int kWaves = 4;
   static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kPer = DV == 256 ? 1 : 2;      // steps of 32 keys to a tile
+  static constexpr int kKeys = 32 * kPer;
+  static constexpr int kDepth = kPer == 2 ? 3 : 4;    // tiles in LDS: one or two in use, the others on their way
   static constexpr int kQueries = 32 * kSets * kWaves;
   static constexpr int kSteps = (DN + P) / 16;
   static constexpr int kKeyCols = DN / 64 + 1, kValueCols = DV / 64;  // groups of 64 columns (the last key group: rope)
   static constexpr int kColBytes = kKeys * 128;
   static constexpr int kTileBytes = (kKeyCols + kValueCols) * kColBytes;
-  static constexpr int kLoads = 8 / kWaves * (kKeyCols + kValueCols);  // of a lane, for a tile
-  static constexpr uint32_t kLds = 2 * kTileBytes;
+  static constexpr int kLoads = kPer * (kKeyCols + kValueCols);  // of a lane, for a tile
+  static constexpr uint32_t kLds = kDepth * kTileBytes;
 };
+
+// Waits for the oldest of the tiles asked for, `later` of which (kLoads loads each) may still be on their way.
+template <int kLoads, int kMost>
+__device__ __forceinline__ void wait_tile(int later) {
+  if constexpr (kMost > 0) {
+    if (later >= kMost) return wait_loads_and_meet<kLoads * kMost>();
+    return wait_tile<kLoads, kMost - 1>(later);
+  }
+  wait_loads_and_meet<0>();
+}
 
 __device__ __forceinline__ int cut(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
@@ -118,7 +130,7 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
     // keys that the workgroup's last query sees, and its part of their tiles
     const int last_q = first + S::kQueries < nq ? first + S::kQueries - 1 : nq - 1;
     const int end = a.causal ? cut(nk - nq + last_q + 1, nk) : nk;
-    const int all = (end + kKeys - 1) / kKeys;
+    const int all = (end + S::kKeys - 1) / S::kKeys;
     const int t0 = (int)((int64_t)all * split / a.splits), t1 = (int)((int64_t)all * (split + 1) / a.splits);
 
     const int wq = first + wave * 32 * kSets;  // the wave's first query
@@ -152,100 +164,173 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       sum[g] = rsum[g] = 0.0f;
     }
 
-    // the lane's chunk of a key (two keys 32 apart) of every tile
+    // the lane's chunk of one key of every tile
     const int mine = 8 * wave + (lane >> 3), place = (lane & 7) ^ swizzle(mine);
     const char* kv = (const char*)a.kv + ((size_t)k0 * a.heads + h) * (2 * (DN + DV)) + 16 * place;
     const char* kr = (const char*)a.krope + (size_t)k0 * a.rope_stride * 2 + 16 * (P == 64 ? place : place & 3);
     const size_t kv_row = (size_t)a.heads * (2 * (DN + DV)), kr_row = (size_t)a.rope_stride * 2;
+    int place_in = 0, place_out = 0;  // of the next tile to load, and to use, of kDepth
     auto load = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < 8 / kWaves; ++i) {
-        const uint32_t to = lds0 + (t & 1) * S::kTileBytes + 1024 * (wave + i * kWaves);
-        const int j = t * kKeys + 8 * i * kWaves + mine;
+      for (int i = 0; i < S::kPer; ++i) {
+        const uint32_t to = lds0 + place_in * S::kTileBytes + 4096 * i + 1024 * wave;
+        const int j = t * S::kKeys + 32 * i + mine;
         const char* p = j < nk ? kv + j * kv_row : (const char*)zero_key + 16 * place;
         const char* r = j < nk ? kr + j * kr_row : (const char*)zero_key;
         load_part<0, S::kColBytes>(p, to, std::make_integer_sequence<int, DN / 64>());
         load_to_lds<0>(r, to + DN / 64 * S::kColBytes);
         load_part<2 * DN, S::kColBytes>(p, to + S::kKeyCols * S::kColBytes, std::make_integer_sequence<int, DV / 64>());
       }
+      place_in = place_in + 1 < S::kDepth ? place_in + 1 : 0;
     };
-    if (t0 < t1) load(t0);
-    for (int t = t0; t < t1; ++t) {
-      wait_loads_and_meet<0>();
-      if (t + 1 < t1) load(t + 1);  // into the tile that every wave has left
-      const char* tile = smem + (t & 1) * S::kTileBytes;
+    // tile t is in LDS for every wave; the one that was used before it is left by all, and loaded anew
+    const char* tile = smem;
+    auto next_tile = [&](int t) {
+      wait_tile<S::kLoads, S::kDepth - 3>(t1 - 1 - t);
+      if (t + S::kDepth - 2 < t1) load(t + S::kDepth - 2);
+      tile = smem + place_out * S::kTileBytes;
+      place_out = place_out + 1 < S::kDepth ? place_out + 1 : 0;
+    };
+
+    f16 s[2][kSets];  // scores of two steps
+    float top[kSets];
+    // what one k-step of the first product of step i adds to its scores
+    constexpr int kSet = 4;  // k-steps whose keys are read before the steps before them are multiplied
+    bf8 k[2][kSet];
+    auto read_keys = [&](const char* at, int from) {
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        const int key = t * kKeys + 32 * blk;
-        if (key >= hi) break;
-        f16 s0[kSets];
+      for (int i = 0; i < kSet; ++i)
+        if (from + i < S::kSteps) k[from / kSet & 1][i] = *(const bf8*)(at + kat[i] + S::kColBytes * (from / kSet));
+    };
+    auto score = [&](f16 (&to)[kSets], int j) {
 #pragma unroll
-        for (int g = 0; g < kSets; ++g) s0[g] = f16{};
-        constexpr int kSet = 4;  // k-steps whose keys are read before the steps before them are multiplied
-        bf8 k[2][kSet];
+      for (int g = 0; g < kSets; ++g)
+        to[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[j / kSet & 1][j % kSet], q[g][j], to[g], 0, 0, 0);
+    };
+    // the masked scores of step i, and their maximum so far
+    auto mask = [&](f16 (&x)[kSets], int i) {
+      if (32 * i + 32 <= lo) return;
 #pragma unroll
-        for (int i = 0; i < kSet; ++i) k[0][i] = *(const bf8*)(tile + kat[i] + 4096 * blk);
+      for (int g = 0; g < kSets; ++g)
 #pragma unroll
-        for (int s = 0; s < S::kSteps; s += kSet) {
+        for (int e = 0; e < 16; ++e)
+          x[g][e] = 32 * i + 8 * (e / 4) + e % 4 + 4 * half < limit[g] ? x[g][e] : -INFINITY;
+    };
+    auto raise = [&]() {
 #pragma unroll
-          for (int i = 0; i < kSet; ++i)
-            if (s + kSet + i < S::kSteps)
-              k[(s / kSet + 1) & 1][i] = *(const bf8*)(tile + kat[i] + S::kColBytes * ((s + kSet + i) >> 2) + 4096 * blk);
+      for (int g = 0; g < kSets; ++g) {
+        const float t = max_of_halves(top[g]) * scale;
+        if (__any(t > m[g] + kSlack)) {
+          const float to = fmaxf(m[g], t);
+          if (__any(m[g] > -INFINITY)) {
+            const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
+            sum[g] *= c;
+            rsum[g] *= c;
 #pragma unroll
-          for (int i = 0; i < kSet; ++i)
-            if (s + i < S::kSteps)
-#pragma unroll
-              for (int g = 0; g < kSets; ++g)
-                s0[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[(s / kSet) & 1][i], q[g][s + i], s0[g], 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        constexpr int kReads = 2;
-        bf8 v[kReads][2];
-        auto read_values = [&](int b) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const char* at = tile + S::kColBytes * (b >> 1) + 4096 * blk + 2048 * j;
-            v[b % kReads][j] = read_across(at + vat[b & 1][0], at + vat[b & 1][1]);
+            for (int b = 0; b < kBlocks; ++b) o[g][b] *= c;
           }
-        };
+          m[g] = to;
+        }
+      }
+    };
+    const int mine_end = (hi + 31) / 32;  // the wave's steps end here; the others' loads and barriers go on
+    // step i with its scores in x; those of step i + 1 go to y
+    auto step = [&](int i, f16 (&x)[kSets], f16 (&y)[kSets]) {
+      const char* values = tile + 4096 * (i % S::kPer);
+      if ((i + 1) % S::kPer == 0 && i + 1 < S::kPer * t1) next_tile((i + 1) / S::kPer);
+      if (i >= mine_end) return;
+      const char* keys = tile + 4096 * ((i + 1) % S::kPer);
+      bf8 p[kSets][2];
+      float m0[kSets];
 #pragma unroll
-        for (int b = 0; b < kReads - 1; ++b) read_values(b);
-        bf8 p[kSets][2];
+      for (int g = 0; g < kSets; ++g) m0[g] = m[g] == -INFINITY ? 0.0f : m[g];
+      const bool more = i + 1 < mine_end && i + 1 < S::kPer * t1;
+      if (more) {
 #pragma unroll
         for (int g = 0; g < kSets; ++g) {
-          if (key + 32 > lo) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              s0[g][i] = key + 8 * (i / 4) + i % 4 + 4 * half < limit[g] ? s0[g][i] : -INFINITY;
-          }
-          float top = s0[g][0];
-#pragma unroll
-          for (int i = 1; i < 16; ++i) top = fmaxf(top, s0[g][i]);
-          top = fmaxf(top, __shfl_xor(top, 32)) * scale;
-          if (__any(top > m[g] + kSlack)) {
-            const float to = fmaxf(m[g], top);
-            if (__any(m[g] > -INFINITY)) {
-              const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
-              sum[g] *= c;
-              rsum[g] *= c;
-#pragma unroll
-              for (int b = 0; b < kBlocks; ++b) o[g][b] *= c;
-            }
-            m[g] = to;
-          }
-          weights(s0[g], scale, m[g] == -INFINITY ? 0.0f : m[g], p[g], sum[g], rsum[g]);
+          y[g] = f16{};
         }
-        // O^T, the values read kReads - 1 blocks ahead of their product
+        read_keys(keys, 0);
+        constexpr int kPairs = 8 * kSets;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          if (b + kReads - 1 < kBlocks) read_values(b + kReads - 1);
+        for (int j = 0; j < S::kSteps; ++j) {
+          if (j % kSet == 0) read_keys(keys, j + kSet);
+          score(y, j);
+          // (the pins keep these between the products around them)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(m0[g]));
 #pragma unroll
-            for (int g = 0; g < kSets; ++g)
-              o[g][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[b % kReads][j], p[g][j], o[g][b], 0, 0, 0);
+          for (int e = j * kPairs / S::kSteps; e < (j + 1) * kPairs / S::kSteps; ++e)
+            weigh_pair(x[e / 8], e % 8 * 2, scale, m0[e / 8], p[e / 8], sum[e / 8], rsum[e / 8]);
+#pragma unroll
+          for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(sum[g]), "+v"(rsum[g]));
           __builtin_amdgcn_sched_barrier(0);
         }
+        mask(y, i + 1);
+      } else {
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) weigh(x[g], scale, m0[g], p[g], sum[g], rsum[g]);
+      }
+      bf8 v[2][2];
+      auto read_values = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const char* at = values + S::kColBytes * (b >> 1) + 2048 * j;
+          v[b & 1][j] = read_across(at + vat[b & 1][0], at + vat[b & 1][1]);
+        }
+      };
+      read_values(0);
+#pragma unroll
+      for (int g = 0; g < kSets; ++g) top[g] = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        if (b + 1 < kBlocks) read_values(b + 1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < kSets; ++g)
+            o[g][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[b & 1][j], p[g][j], o[g][b], 0, 0, 0);
+        // (behind the wave's last step these are old scores, and not used)
+#pragma unroll
+        for (int e = b * 16 / kBlocks; e < (b + 1) * 16 / kBlocks; ++e)
+#pragma unroll
+          for (int g = 0; g < kSets; ++g) top[g] = fmaxf(top[g], y[g][e]);
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(top[g]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) raise();
+    };
+
+    if (t0 < t1) {
+#pragma unroll
+      for (int i = 0; i < S::kDepth - 2; ++i)
+        if (t0 + i < t1) load(t0 + i);
+      next_tile(t0);
+      const int begin = S::kPer * t0;
+      if (begin < mine_end) {
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) s[0][g] = f16{};
+        const char* keys = tile;
+        read_keys(keys, 0);
+#pragma unroll
+        for (int j = 0; j < S::kSteps; ++j) {
+          if (j % kSet == 0) read_keys(keys, j + kSet);
+          score(s[0], j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        mask(s[0], begin);
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+          top[g] = s[0][g][0];
+#pragma unroll
+          for (int e = 1; e < 16; ++e) top[g] = fmaxf(top[g], s[0][g][e]);
+        }
+        raise();
+      }
+      for (int i = begin; i < S::kPer * t1; i += 2) {
+        step(i, s[0], s[1]);
+        if (i + 1 < S::kPer * t1) step(i + 1, s[1], s[0]);
       }
     }
     asm volatile("s_barrier" ::: "memory");  // every wave has left the tiles
@@ -316,7 +401,7 @@ __global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
   }
 }
 
-constexpr int sets_of(int) { return 1; }
+constexpr int sets_of(int value) { return value == 256 ? 1 : 2; }
 
 template <int DN, int P, int DV>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
