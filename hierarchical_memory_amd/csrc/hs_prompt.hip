@@ -216,21 +216,28 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
         for (int e = 0; e < 16; ++e)
           x[g][e] = 32 * i + 8 * (e / 4) + e % 4 + 4 * half < limit[g] ? x[g][e] : -INFINITY;
     };
+    // whether the maximum moves by the scores of a step, and its move
+    auto raises = [&]() {
+      bool any = false;
+#pragma unroll
+      for (int g = 0; g < kSets; ++g) {
+        top[g] = max_of_halves(top[g]) * scale;
+        any |= top[g] > m[g] + kSlack;
+      }
+      return __any(any);
+    };
     auto raise = [&]() {
 #pragma unroll
       for (int g = 0; g < kSets; ++g) {
-        const float t = max_of_halves(top[g]) * scale;
-        if (__any(t > m[g] + kSlack)) {
-          const float to = fmaxf(m[g], t);
-          if (__any(m[g] > -INFINITY)) {
-            const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
-            sum[g] *= c;
-            rsum[g] *= c;
+        const float to = top[g] > m[g] + kSlack ? top[g] : m[g];
+        const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
+        if (__any(m[g] > -INFINITY && c != 1.0f)) {
+          sum[g] *= c;
+          rsum[g] *= c;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) o[g][b] *= c;
-          }
-          m[g] = to;
+          for (int b = 0; b < kBlocks; ++b) o[g][b] *= c;
         }
+        m[g] = to;
       }
     };
     const int mine_end = (hi + 31) / 32;  // the wave's steps end here; the others' loads and barriers go on
@@ -244,62 +251,71 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       float m0[kSets];
 #pragma unroll
       for (int g = 0; g < kSets; ++g) m0[g] = m[g] == -INFINITY ? 0.0f : m[g];
-      const bool more = i + 1 < mine_end && i + 1 < S::kPer * t1;
-      if (more) {
-#pragma unroll
-        for (int g = 0; g < kSets; ++g) {
-          y[g] = f16{};
-        }
-        read_keys(keys, 0);
-        constexpr int kPairs = 8 * kSets;
-#pragma unroll
-        for (int j = 0; j < S::kSteps; ++j) {
-          if (j % kSet == 0) read_keys(keys, j + kSet);
-          score(y, j);
-          // (the pins keep these between the products around them)
-#pragma unroll
-          for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(m0[g]));
-#pragma unroll
-          for (int e = j * kPairs / S::kSteps; e < (j + 1) * kPairs / S::kSteps; ++e)
-            weigh_pair(x[e / 8], e % 8 * 2, scale, m0[e / 8], p[e / 8], sum[e / 8], rsum[e / 8]);
-#pragma unroll
-          for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(sum[g]), "+v"(rsum[g]));
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        mask(y, i + 1);
-      } else {
-#pragma unroll
-        for (int g = 0; g < kSets; ++g) weigh(x[g], scale, m0[g], p[g], sum[g], rsum[g]);
-      }
-      bf8 v[2][2];
+      constexpr int kReads = 3;  // blocks of values that are read before the products of the block before them end
+      bf8 v[kReads][2];
       auto read_values = [&](int b) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const char* at = values + S::kColBytes * (b >> 1) + 2048 * j;
-          v[b & 1][j] = read_across(at + vat[b & 1][0], at + vat[b & 1][1]);
+          v[b % kReads][j] = read_across(at + vat[b & 1][0], at + vat[b & 1][1]);
         }
       };
-      read_values(0);
+      const bool more = i + 1 < mine_end && i + 1 < S::kPer * t1;
+      if (more) {
+        constexpr int kPairs = 8 * kSets, kFirst = kPairs / 4;  // weights, and those before the keys are here
+        auto weigh_some = [&](int from, int to) {
+          // (the pins keep them between the products around them)
 #pragma unroll
-      for (int g = 0; g < kSets; ++g) top[g] = -INFINITY;
+          for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(m0[g]));
+#pragma unroll
+          for (int e = from; e < to; ++e)
+            weigh_pair(x[e / 8], e % 8 * 2, scale, m0[e / 8], p[e / 8], sum[e / 8], rsum[e / 8]);
+#pragma unroll
+          for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(sum[g]), "+v"(rsum[g]));
+          __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) y[g] = f16{};
+        read_keys(keys, 0);
+        weigh_some(0, kFirst);
+#pragma unroll
+        for (int j = 0; j < S::kSteps; ++j) {
+          if (j % kSet == 0) read_keys(keys, j + kSet);
+          if (j == S::kSteps - kSet) read_values(0);
+          if (j == S::kSteps - kSet / 2) read_values(1);
+          score(y, j);
+          weigh_some(kFirst + j * (kPairs - kFirst) / S::kSteps, kFirst + (j + 1) * (kPairs - kFirst) / S::kSteps);
+        }
+        mask(y, i + 1);
+      } else {
+        read_values(0);
+        read_values(1);
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) weigh(x[g], scale, m0[g], p[g], sum[g], rsum[g]);
+      }
+      bool up = false;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        if (b + 1 < kBlocks) read_values(b + 1);
+        if (b + 2 < kBlocks) read_values(b + 2);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int g = 0; g < kSets; ++g)
-            o[g][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[b & 1][j], p[g][j], o[g][b], 0, 0, 0);
-        // (behind the wave's last step these are old scores, and not used)
+            o[g][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[b % kReads][j], p[g][j], o[g][b], 0, 0, 0);
+        // the maximum of the scores (behind the wave's last step they are old ones, and it is not used)
+        if (b == 0) {
 #pragma unroll
-        for (int e = b * 16 / kBlocks; e < (b + 1) * 16 / kBlocks; ++e)
+          for (int g = 0; g < kSets; ++g) {
+            top[g] = y[g][0];
 #pragma unroll
-          for (int g = 0; g < kSets; ++g) top[g] = fmaxf(top[g], y[g][e]);
-#pragma unroll
-        for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(top[g]));
+            for (int e = 1; e < 16; ++e) top[g] = fmaxf(top[g], y[g][e]);
+            asm volatile("" : "+v"(top[g]));
+          }
+        }
+        if (b == 1) up = raises();
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) raise();
+      if (more && up) raise();
     };
 
     if (t0 < t1) {
@@ -326,7 +342,7 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
 #pragma unroll
           for (int e = 1; e < 16; ++e) top[g] = fmaxf(top[g], s[0][g][e]);
         }
-        raise();
+        if (raises()) raise();
       }
       for (int i = begin; i < S::kPer * t1; i += 2) {
         step(i, s[0], s[1]);
