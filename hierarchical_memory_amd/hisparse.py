@@ -384,42 +384,86 @@ def hs_row_bytes(fmt: HsRowFormat) -> int:
     return n.value
 
 
-def _on_device(*tensors) -> None:
-    """Refuses a tensor of another GPU than the current one (the library checks that this is the context's)."""
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != dev:
-            raise ValueError(f"expected a tensor on the current device (cuda:{dev}), got one on {t.device}")
+# The latent-attention calls are short, and a decode step makes several: their checks are one expression over the
+# tensors' metadata each, and the functions below say which of them failed only when one did.
+_torch = None
 
 
-def _typed(name: str, t, dtype, shape=None, nullable: bool = False):
-    """A contiguous tensor argument of one dtype and shape (None in the shape: any size), or None where it may be."""
-    if t is None:
-        if nullable:
-            return None
-        raise ValueError(f"{name} must not be None")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    return t
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _current(dev: int) -> int:
+    """Index of the current device (-1 for a call whose first tensor is on the CPU)."""
+    return _t()._C._cuda_getDevice() if dev >= 0 else -1
+
+
+def _refuse(dev: int, *checks) -> None:
+    """Raises for the first of the checks (name, tensor, dtype, shape or least element count, nullable) that fails."""
+    for name, t, dtype, shape, nullable in checks:
+        if t is None:
+            if nullable:
+                continue
+            raise ValueError(f"{name} must not be None")
+        if dtype is not None and t.dtype is not dtype:
+            raise ValueError(f"{name} must be a {dtype} tensor, got {t.dtype}")
+        if isinstance(shape, int):
+            if t.numel() < shape:
+                raise ValueError(f"{name} has {t.numel()} elements, the context needs at least {shape}")
+        elif shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    for name, t, _, _, _ in checks:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"expected a GPU tensor, got one on {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected a tensor on the current device (cuda:{dev}), {name} is on {t.device}")
+        if t is not None and not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+    raise ValueError("bad arguments")
+
+
+def _i32_fine(t, n: int, dev: int) -> bool:
+    return t is not None and t.dtype is _torch.int32 and t.numel() >= n and t.get_device() == dev and t.is_contiguous()
+
+
+def _fine(t, dtype, shape, dev: int) -> bool:
+    return t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _at(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def hs_map_tokens(ctx, new, length, tail0, cu, req, pos, slot, status=None, stream=None) -> None:
     """new, length: device int32 [R], new and present tokens of each request; tail0 [R] where the context has a tail,
     else None. Outputs: cu [R + 1], and req, pos, slot of one length, the most tokens that the map takes."""
-    lim = _lim(ctx)
+    i32 = _t().int32
+    lim = _CTX_SIZES.get(_ctx_key(ctx))
     R = lim.R if lim is not None else 0
     n = req.numel() if req is not None else 0
-    for name, t in (("pos", pos), ("slot", slot)):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"req and {name} must have one length, got {n} and {t.numel()}")
-    _on_device(new, length, tail0, cu, req, pos, slot, status)
-    a = _ptrs(_arg("new", new, lim, R), _arg("length", length, lim, R), _arg("tail0", tail0, lim, R, nullable=True),
-              _arg("cu", cu, lim, R + 1), _arg("req", req, lim), _arg("pos", pos, lim), _arg("slot", slot, lim),
-              _arg("status", status, lim, R, nullable=True))
-    _check(lib().hs_map_tokens(ctx, *a[:3], n, *a[3:], _stream(stream)))
+    dev = new.get_device() if new is not None else -1
+    if not (_i32_fine(new, R, dev) and _i32_fine(length, R, dev) and _i32_fine(cu, R + 1, dev)
+            and _i32_fine(req, n, dev) and _i32_fine(pos, n, dev) and _i32_fine(slot, n, dev)
+            and (tail0 is None or _i32_fine(tail0, R, dev)) and (status is None or _i32_fine(status, R, dev))
+            and pos.numel() == n and slot.numel() == n and dev >= 0 and dev == _torch._C._cuda_getDevice()):
+        for name, t in (("pos", pos), ("slot", slot)):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"req and {name} must have one length, got {n} and {t.numel()}")
+        _refuse(_current(dev), ("new", new, i32, R, False), ("length", length, i32, R, False),
+                ("tail0", tail0, i32, R, True), ("cu", cu, i32, R + 1, False), ("req", req, i32, n, False),
+                ("pos", pos, i32, n, False), ("slot", slot, i32, n, False), ("status", status, i32, R, True))
+    _check(lib().hs_map_tokens(ctx, new.data_ptr(), length.data_ptr(), _at(tail0), n, cu.data_ptr(), req.data_ptr(),
+                               pos.data_ptr(), slot.data_ptr(), _at(status), _raw_stream(stream, dev)))
 
 
 def hs_store_rows(ctx, fmt: HsRowFormat, x, weight, eps: float, freqs, req, pos, slot, latent=None,
@@ -427,23 +471,32 @@ def hs_store_rows(ctx, fmt: HsRowFormat, x, weight, eps: float, freqs, req, pos,
     """x: device bf16 [n, latent + rope], rows of any stride that is a multiple of 8 (a slice of a wider projection);
     weight: bf16 [latent]; freqs: float64 [rope / 2] or None; req, pos, slot: int32 [n] as hs_map_tokens wrote them;
     latent: bf16 [n, latent + rope] output or None."""
-    import torch
-    lim = _lim(ctx)
-    _typed("x", x, torch.bfloat16, (None, fmt.latent + fmt.rope))
-    n = x.shape[0]
-    if x.stride(1) != 1:
+    t = _t()
+    bf16, i32 = t.bfloat16, t.int32
+    lim = _CTX_SIZES.get(_ctx_key(ctx))
+    R = lim.R if lim is not None else 0
+    L, P = fmt.latent, fmt.rope
+    if x is None:
+        raise ValueError("x must not be None")
+    if x.dtype is not bf16:
+        raise ValueError(f"x must be a {bf16} tensor, got {x.dtype}")
+    if x.dim() != 2 or x.shape[1] != L + P:
+        raise ValueError(f"x must have shape [n, {L + P}], got {list(x.shape)}")
+    n, (step, one) = x.shape[0], x.stride()
+    if one != 1:
         raise ValueError("x must have contiguous rows")
-    _typed("weight", weight, torch.bfloat16, (fmt.latent,))
-    _typed("freqs", freqs, torch.float64, (fmt.rope // 2,), nullable=True)
-    _typed("latent", latent, torch.bfloat16, (n, fmt.latent + fmt.rope), nullable=True)
-    if not x.is_cuda:
-        raise ValueError(f"expected a GPU tensor, got one on {x.device}")
-    _on_device(x, weight, freqs, req, pos, slot, latent, status)
-    w, f, r, p, s, o, st = _ptrs(weight, freqs, _typed("req", req, torch.int32, (n,)),
-                                 _typed("pos", pos, torch.int32, (n,)), _typed("slot", slot, torch.int32, (n,)), latent,
-                                 _arg("status", status, lim, lim.R if lim is not None else 0, nullable=True))
-    _check(lib().hs_store_rows(ctx, ctypes.byref(fmt), x.data_ptr(), x.stride(0) if n > 1 else x.shape[1], w, eps, f,
-                               rope_style, r, p, s, n, o, st, _stream(stream)))
+    dev = x.get_device()
+    if not (_fine(weight, bf16, (L,), dev) and (freqs is None or _fine(freqs, t.float64, (P // 2,), dev))
+            and _fine(req, i32, (n,), dev) and _fine(pos, i32, (n,), dev) and _fine(slot, i32, (n,), dev)
+            and (latent is None or _fine(latent, bf16, (n, L + P), dev))
+            and (status is None or _i32_fine(status, R, dev)) and dev >= 0 and dev == t._C._cuda_getDevice()):
+        _refuse(_current(dev), ("weight", weight, bf16, (L,), False), ("freqs", freqs, t.float64, (P // 2,), True),
+                ("req", req, i32, (n,), False), ("pos", pos, i32, (n,), False), ("slot", slot, i32, (n,), False),
+                ("latent", latent, bf16, (n, L + P), True), ("status", status, i32, R, True),
+                ("x", x[:0], None, None, False))
+    _check(lib().hs_store_rows(ctx, ctypes.byref(fmt), x.data_ptr(), step if n > 1 else L + P, weight.data_ptr(), eps,
+                               _at(freqs), rope_style, req.data_ptr(), pos.data_ptr(), slot.data_ptr(), n, _at(latent),
+                               _at(status), _raw_stream(stream, dev)))
 
 
 def hs_attend_work_bytes(cfg: HsConfig, fmt: HsRowFormat, heads: int) -> int:
@@ -456,17 +509,30 @@ def hs_attend(ctx, fmt: HsRowFormat, q, scale: float, out, o, lse=None, gather=N
     """q: device bf16 [R, heads, latent + rope]; out: int32 [R, k] as a resolve or trial wrote it; gather: None (rows in
     place) or the gathered rows; o: bf16 [R, heads, latent]; lse: float32 [R, heads] or None; work: a device buffer of
     hs_attend_work_bytes."""
-    import torch
-    lim = _lim(ctx)
-    _typed("q", q, torch.bfloat16, (lim.R if lim is not None else None, None, fmt.latent + fmt.rope))
-    heads = q.shape[1]
-    _typed("o", o, torch.bfloat16, (q.shape[0], heads, fmt.latent))
-    _typed("lse", lse, torch.float32, (q.shape[0], heads), nullable=True)
-    _on_device(q, out, o, lse, gather, work)
-    a = _ptrs(q, _arg("out", out, lim, lim.RK if lim is not None else 0),
-              _arg("gather", gather, lim, nbytes=lim.gather if lim is not None else 0, int32=False, nullable=True),
-              o, lse, work)
-    _check(lib().hs_attend(ctx, ctypes.byref(fmt), a[0], heads, scale, *a[1:], _bytes(work), _stream(stream)))
+    t = _t()
+    bf16, f32 = t.bfloat16, t.float32
+    lim = _CTX_SIZES.get(_ctx_key(ctx))
+    L, D = fmt.latent, fmt.latent + fmt.rope
+    if q is None:
+        raise ValueError("q must not be None")
+    if q.dim() != 3 or q.shape[2] != D or (lim is not None and q.shape[0] != lim.R):
+        raise ValueError(f"q must have shape [{lim.R if lim is not None else 'R'}, heads, {D}], got {list(q.shape)}")
+    R, heads, _ = q.shape
+    need, rows = (lim.RK, lim.gather) if lim is not None else (0, 0)
+    dev = q.get_device()
+    if not (q.dtype is bf16 and q.is_contiguous() and _i32_fine(out, need, dev) and _fine(o, bf16, (R, heads, L), dev)
+            and (lse is None or _fine(lse, f32, (R, heads), dev))
+            and (gather is None or (gather.numel() * gather.element_size() >= rows and gather.get_device() == dev
+                                    and gather.is_contiguous()))
+            and (work is None or (work.get_device() == dev and work.is_contiguous()))
+            and dev >= 0 and dev == t._C._cuda_getDevice()):
+        if gather is not None and gather.numel() * gather.element_size() < rows:
+            raise ValueError(f"gather has {_bytes(gather)} bytes, the context needs at least {rows}")
+        _refuse(_current(dev), ("q", q, bf16, None, False), ("out", out, t.int32, need, False),
+                ("o", o, bf16, (R, heads, L), False), ("lse", lse, f32, (R, heads), True),
+                ("gather", gather, None, None, True), ("work", work, None, None, True))
+    _check(lib().hs_attend(ctx, ctypes.byref(fmt), q.data_ptr(), heads, scale, out.data_ptr(), _at(gather), o.data_ptr(),
+                           _at(lse), _at(work), _bytes(work), _raw_stream(stream, dev)))
 
 
 def hs_attend_prompt_work_bytes(num_requests: int, n_q: int, n_k: int, heads: int, nope: int, rope: int,
@@ -482,35 +548,46 @@ def hs_attend_prompt(ctx, q, kv, rope, cu_q, cu_k, scale: float, o, lse=None, ca
     any stride that is a multiple of 8 (the rope columns of the latent rows); cu_q, cu_k: int32 [R + 1];
     o: bf16 [n_q, heads, value]; lse: float32 [n_q, heads] or None; work: a device buffer of hs_attend_prompt_work_bytes,
     or None: one is taken from torch's allocator for the call where it takes one (on the call's stream)."""
-    import torch
-    lim = _lim(ctx)
+    t = _t()
+    bf16, f32, i32 = t.bfloat16, t.float32, t.int32
+    lim = _CTX_SIZES.get(_ctx_key(ctx))
     R = lim.R if lim is not None else 0
-    _typed("q", q, torch.bfloat16, (None, None, None))
-    n_q, heads, dq = q.shape
-    _typed("kv", kv, torch.bfloat16, (None, heads, None))
-    n_k = kv.shape[0]
-    _typed("rope", rope, torch.bfloat16, (n_k, None))
-    dr = rope.shape[1]
-    if rope.stride(1) != 1 and n_k > 0:
-        raise ValueError("rope must have contiguous rows")
-    _typed("o", o, torch.bfloat16, (n_q, heads, None))
-    value = o.shape[2]
+    for name, x, dims in (("q", q, 3), ("kv", kv, 3), ("rope", rope, 2), ("o", o, 3)):
+        if x is None:
+            raise ValueError(f"{name} must not be None")
+        if x.dtype is not bf16:
+            raise ValueError(f"{name} must be a {bf16} tensor, got {x.dtype}")
+        if x.dim() != dims:
+            raise ValueError(f"{name} must have shape of {dims} dimensions, got {list(x.shape)}")
+    (n_q, heads, dq), (n_k, kv_heads, dkv), (n_rope, dr), value = q.shape, kv.shape, rope.shape, o.shape[2]
     nope = dq - dr
-    if kv.shape[2] != nope + value:
-        raise ValueError(f"kv must hold {nope} + {value} values a head (q's without rope, and o's), got {kv.shape[2]}")
-    _typed("lse", lse, torch.float32, (n_q, heads), nullable=True)
-    if not rope.is_cuda:
-        raise ValueError(f"expected a GPU tensor, got one on {rope.device}")
-    _on_device(q, kv, rope, cu_q, cu_k, o, lse, work)
+    if kv_heads != heads:
+        raise ValueError(f"kv must have shape [n_k, {heads}, nope + value], got {list(kv.shape)}")
+    if n_rope != n_k:
+        raise ValueError(f"rope must have shape [{n_k}, rope], got {list(rope.shape)}")
+    if dkv != nope + value:
+        raise ValueError(f"kv must hold {nope} + {value} values a head (q's without rope, and o's), got {dkv}")
+    step, one = rope.stride()
+    if one != 1 and n_k > 0:
+        raise ValueError("rope must have contiguous rows")
+    dev = q.get_device()
+    if not (q.is_contiguous() and kv.is_contiguous() and kv.get_device() == dev and rope.get_device() == dev
+            and _i32_fine(cu_q, R + 1, dev) and _i32_fine(cu_k, R + 1, dev) and _fine(o, bf16, (n_q, heads, value), dev)
+            and (lse is None or _fine(lse, f32, (n_q, heads), dev))
+            and (work is None or (work.get_device() == dev and work.is_contiguous()))
+            and dev >= 0 and dev == t._C._cuda_getDevice()):
+        _refuse(_current(dev), ("q", q, bf16, None, False), ("kv", kv, bf16, None, False),
+                ("rope", rope[:0], bf16, None, False), ("cu_q", cu_q, i32, R + 1, False),
+                ("cu_k", cu_k, i32, R + 1, False), ("o", o, bf16, (n_q, heads, value), False),
+                ("lse", lse, f32, (n_q, heads), True), ("work", work, None, None, True))
     if work is None and lim is not None:
         n = hs_attend_prompt_work_bytes(R, n_q, n_k, heads, nope, dr, value)
         if n:
-            with torch.cuda.stream(_torch_stream(stream)):
-                work = torch.empty((n,), dtype=torch.uint8, device=q.device)
-    pq, pkv, pcq, pck, po, pl, pw = _ptrs(q, kv, _arg("cu_q", cu_q, lim, R + 1), _arg("cu_k", cu_k, lim, R + 1), o, lse,
-                                          work)
-    _check(lib().hs_attend_prompt(ctx, pq, pkv, rope.data_ptr(), rope.stride(0) if n_k > 1 else dr, pcq, pck, n_q, n_k,
-                                  heads, nope, dr, value, scale, int(causal), po, pl, pw, _bytes(work), _stream(stream)))
+            with t.cuda.stream(_torch_stream(stream)):
+                work = t.empty((n,), dtype=t.uint8, device=q.device)
+    _check(lib().hs_attend_prompt(ctx, q.data_ptr(), kv.data_ptr(), rope.data_ptr(), step if n_k > 1 else dr,
+                                  cu_q.data_ptr(), cu_k.data_ptr(), n_q, n_k, heads, nope, dr, value, scale, int(causal),
+                                  o.data_ptr(), _at(lse), _at(work), _bytes(work), _raw_stream(stream, dev)))
 
 
 def hs_rebuild_order(ctx, stream=None) -> None:
