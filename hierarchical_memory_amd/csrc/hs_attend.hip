@@ -3,14 +3,14 @@
 //
 //   s = scale * q . row,   o = sum_j p_j latent_j / sum_j p_j,   p_j = 2^(s_j log2 e - m)   (m a running maximum)
 //
-// One pass over the rows, 32 to a tile. A workgroup of four waves takes a part of one request's selection and 32, 64 or
-// 128 of its heads; it reads each row once, whatever the number of heads. Matrix instructions do both products
-// transposed, so that a head is a lane's column in both and its maximum, sum and rescaling stay inside the lane:
+// One pass over the rows, 32 to a tile. A workgroup of eight waves, two to a SIMD, takes a part of one request's selection
+// and up to 128 of its heads; it reads each row once, whatever the number of heads. Matrix instructions do both products
+// transposed, so that a head is a lane's column in both and its maximum, sum and rescaling stay inside four lanes:
 //   S^T[key][head]  = K Q^T     A: the tile's rows from LDS, B: the queries, kept in registers
 //   O^T[dim][head] += V^T P^T   A: the same rows read through the transposing LDS load, B: the weights as S^T left them
-// (a lane half h holds the keys 8 i + 4 h + 0..3 of S^T; the second product takes its keys in that order, so the weights
-// never change lanes). With w head groups of 32 the other 4 / w waves of a group share out the latent dimensions of the
-// second product and each repeat the first.
+// (lane group g = lane / 16 holds the keys 4 g + 0..3 and 16 + 4 g + 0..3 of S^T; the second product takes its keys in that
+// order, so the weights never change lanes). With fewer than eight groups of 16 heads the waves of a group share out the
+// latent dimensions of the second product and each repeat the first.
 #include "hs_latent.h"
 #include "hs_mfma.h"
 
@@ -21,12 +21,20 @@ namespace hs {
 
 namespace {
 
-constexpr int kAttendThreads = 256;
+constexpr int kAttendThreads = 512;
+constexpr int kWavesA = kAttendThreads / 64;
 constexpr int kTile = 32;          // rows of a tile
 constexpr int kDepth = 4;          // tiles in LDS as memory has them: one in use, the others on their way
 constexpr int kListed = 1024;      // rows of the selection whose indices are held in LDS at a time
 constexpr int kGroupHeads = 128;   // most heads of one workgroup
+constexpr int kMostSplits = 64;    // parts of a selection: one to a lane of the wave that joins them
 __device__ __align__(16) uint4 zero_row[72];  // what a tile holds where there is no row
+
+// A tile's chunks change places by the row (see hs_mfma.h). LDS answers a 16-byte read in four steps, the first for the lanes
+// 0-3, 12-15, 20-23 and 24-27: rows 0-3 and 12-15 at one chunk and rows 4-11 at its neighbour. Those, and 8 rows at two
+// neighbouring chunks, meet no bank twice (256 requests x 2048 rows x 128 heads: 185 us with an order that is free of
+// conflicts only where all 16 rows are read at one chunk, 172 us with this).
+__device__ __forceinline__ int swizzle16(int row) { return (((row >> 1) & 3) << 1) ^ (((row >> 3) & 1) * 5); }
 
 template <int L, int P, bool kMx>
 struct Shape {
@@ -34,35 +42,58 @@ struct Shape {
   static constexpr int kCols = (D + 63) / 64;              // groups of columns of a tile in bf16
   static constexpr int kColBytes = kTile * 128;
   static constexpr int kTileBytes = kCols * kColBytes;
-  static constexpr int kSteps = D / 16;                    // of the first product
+  static constexpr int kSteps = D / 32;                    // of the first product
   // an 8-bit row as memory has it, in groups of 128 bytes and what is left of it (1 or 5 chunks)
   static constexpr int kScales = L, kRope = L + (L / kScaleBlock + 15) / 16 * 16, kRowBytes = kRope + 2 * P;
   static constexpr int kRawCols = kRowBytes / 128, kRawRest = kRowBytes / 16 % 8;
   static constexpr int kRawBytes = kTile * kRowBytes;
-  static constexpr int kLoads = kMx ? kRawCols + 1 : kCols;  // of a lane, for a tile
+  // loads of a lane for a tile: the first four waves take its even groups, the others the odd ones and the rest
+  static constexpr int kEven = ((kMx ? kRawCols : kCols) + 1) / 2;
+  static constexpr int kOdd = (kMx ? kRawCols : kCols) / 2 + (kMx ? 1 : 0);
   static constexpr int kAhead = kMx ? kDepth : kDepth - 1;   // tiles asked for before the one in use
-  static constexpr uint32_t kLds = (kMx ? 2 * kTileBytes + kDepth * kRawBytes : kDepth * kTileBytes) + 4 * kListed;
+  static constexpr int kLoadBytes = kMx ? kRawBytes : kTileBytes;
+  static constexpr uint32_t kLds = (kMx ? 2 * kTileBytes : 0) + kDepth * kLoadBytes + 4 * kListed;
   static_assert(!kMx || kRawRest > 0, "the rest is a load of its own");
+  static_assert((kMx ? 2 * kTileBytes : 0) + kDepth * kLoadBytes >= 4 * kTileBytes, "room for the queries of 128 heads");
 };
 
-// The loads of one lane for a tile: its chunk of every group of 128 bytes, `row` the address of that chunk in the first.
-// bf16 rows of 32 rope values end inside a group: there `last` keeps to the row's end.
-template <bool kHalf, int kGroupBytes, int... G>
+// The loads of one lane for every second group of 128 bytes of a tile from kFirst on: its chunk of each, `row` the address
+// of that chunk in the first group. Rows of 32 rope values in bf16 end inside a group: there `last` keeps to the row's end.
+template <int kFirst, int kCols, bool kHalf, int kGroupBytes, int... G>
 __device__ __forceinline__ void load_groups(const char* row, const char* last, uint32_t lds,
                                             std::integer_sequence<int, G...>) {
-  (load_to_lds<128 * G>(kHalf && G == (int)sizeof...(G) - 1 ? last : row, lds + G * kGroupBytes), ...);
+  (load_to_lds<128 * (2 * G + kFirst)>(kHalf && 2 * G + kFirst == kCols - 1 ? last : row,
+                                       lds + (2 * G + kFirst) * kGroupBytes),
+   ...);
+}
+
+template <int kCols, bool kHalf, int kGroupBytes>
+__device__ __forceinline__ void load_half(bool odd, const char* row, const char* last, uint32_t lds) {
+  if (odd)
+    load_groups<1, kCols, kHalf, kGroupBytes>(row, last, lds, std::make_integer_sequence<int, kCols / 2>());
+  else
+    load_groups<0, kCols, kHalf, kGroupBytes>(row, last, lds, std::make_integer_sequence<int, (kCols + 1) / 2>());
 }
 
 struct Part { int r, split, h0, begin, end; };
 
 __device__ __forceinline__ Part part_of(const AttendArgs& a) {
   Part p;
-  int b = blockIdx.x;
   const int groups = (a.heads + kGroupHeads - 1) / kGroupHeads;
-  p.split = b % a.splits;
-  b /= a.splits;
-  p.h0 = b % groups * kGroupHeads;
-  p.r = b / groups;
+  // Workgroups go round the eight chiplets in turn. The parts of one request and its queries stay on one, whose cache then
+  // gets the queries once: of every eight requests (and head groups) one to a chiplet, those behind the last eight as they come.
+  int b = blockIdx.x, u;
+  const int whole = a.R * groups / 8 * 8;
+  if (b < whole * a.splits) {
+    p.split = b / 8 % a.splits;
+    u = b / 8 / a.splits * 8 + b % 8;
+  } else {
+    b -= whole * a.splits;
+    p.split = b % a.splits;
+    u = whole + b / a.splits;
+  }
+  p.h0 = u % groups * kGroupHeads;
+  p.r = u / groups;
   // parts in whole tiles, as even as they come
   const int tiles = (a.k + kTile - 1) / kTile;
   const int per = tiles / a.splits, more = tiles % a.splits;
@@ -73,54 +104,71 @@ __device__ __forceinline__ Part part_of(const AttendArgs& a) {
   return p;
 }
 
-// A raw tile of 8-bit rows to bf16: thread (row, c) takes 16 values of each 128, their scale's byte from the row, and the
+// A raw tile of 8-bit rows to bf16: thread (row, c) takes 16 values of each 256, their scale's byte from the row, and the
 // row's c-th chunk of rope values. Values times a power of two are exact in bf16.
 template <int L, int P>
-__device__ __forceinline__ void convert_tile(const char* raw, char* tile, int tid) {
+struct Converter {
   using S = Shape<L, P, true>;
-  const int row = tid >> 3, c = tid & 7, f = swizzle(row);
-  auto chunk = [&](int q) {  // of the row, which may lie in its rest
-    return q < 8 * S::kRawCols ? raw + (q >> 3) * S::kColBytes + row * 128 + (q & 7) * 16
-                               : raw + S::kRawCols * S::kColBytes + (row * S::kRawRest + q - 8 * S::kRawCols) * 16;
-  };
-  const v4u scales = *(const v4u*)chunk(S::kScales / 16);
-#pragma unroll
-  for (int j = 0; j < L / 128; ++j) {
-    const v4u x = *(const v4u*)(raw + j * S::kColBytes + row * 128 + c * 16);
-    const float scale = __uint_as_float(((scales[j] >> (8 * (c >> 1))) & 255u) << 23);
-    v4u y[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i / 2][i % 2 * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], scale, false));
-      y[i / 2][i % 2 * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], scale, true));
-    }
-    // the two halves of a row's eight threads write to two groups of columns: in opposite order, to other banks
-    char* to = tile + (2 * j + (c >> 2)) * S::kColBytes + row * 128;
-    const int first = c >> 2;
-    *(v4u*)(to + (((2 * (c & 3) + first) ^ f) << 4)) = first ? y[1] : y[0];
-    *(v4u*)(to + (((2 * (c & 3) + 1 - first) ^ f) << 4)) = first ? y[0] : y[1];
-  }
-  if (c < P / 8) {
-    *(v4u*)(tile + L / 64 * S::kColBytes + row * 128 + ((c ^ f) << 4)) = *(const v4u*)chunk(S::kRope / 16 + c);
-  }
-}
+  v4u values[L / 256], rope;
+  uint32_t scales[L / 256];
 
-// kGroups: head groups of 32 (1, 2 or 4).
+  __device__ __forceinline__ void read(const char* raw, int tid) {
+    const int row = tid >> 4, c = tid & 15;
+    auto chunk = [&](int q) {  // of the row, which may lie in its rest
+      return q < 8 * S::kRawCols ? raw + (q >> 3) * S::kColBytes + row * 128 + (q & 7) * 16
+                                 : raw + S::kRawCols * S::kColBytes + (row * S::kRawRest + q - 8 * S::kRawCols) * 16;
+    };
+#pragma unroll
+    for (int j = 0; j < L / 256; ++j) {
+      values[j] = *(const v4u*)chunk(16 * j + c);
+      scales[j] = ((const uint32_t*)chunk(S::kScales / 16))[2 * j + (c >> 3)];
+    }
+    rope = *(const v4u*)chunk(S::kRope / 16 + (c & (P / 8 - 1)));
+  }
+
+  __device__ __forceinline__ void write(char* tile, int tid) const {
+    const int row = tid >> 4, c = tid & 15, f = swizzle16(row);
+#pragma unroll
+    for (int j = 0; j < L / 256; ++j) {
+      const float scale = __uint_as_float(((scales[j] >> (8 * ((c >> 1) & 3))) & 255u) << 23);
+      v4u y[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = values[j][i];
+        y[i / 2][i % 2 * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, false));
+        y[i / 2][i % 2 * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, true));
+      }
+      // neighbouring groups of columns in opposite order, to other banks
+      char* to = tile + (4 * j + (c >> 2)) * S::kColBytes + row * 128;
+      const int first = (c >> 2) & 1;
+      *(v4u*)(to + (((2 * (c & 3) + first) ^ f) << 4)) = first ? y[1] : y[0];
+      *(v4u*)(to + (((2 * (c & 3) + 1 - first) ^ f) << 4)) = first ? y[0] : y[1];
+    }
+    if (c < P / 8) *(v4u*)(tile + L / 64 * S::kColBytes + row * 128 + ((c ^ f) << 4)) = rope;
+  }
+};
+template <>
+struct Converter<0, 0> {
+  __device__ __forceinline__ void read(const char*, int) {}
+  __device__ __forceinline__ void write(char*, int) const {}
+};
+
+// kGroups: head groups of 16 (1, 2, 4 or 8).
 template <int L, int P, bool kMx, int kGroups>
-__global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   using S = Shape<L, P, kMx>;
-  constexpr int kShare = 4 / kGroups;            // waves that share out a head group's dimensions
-  constexpr int kBlocks = L / 32 / kShare;       // blocks of 32 dimensions of a wave
-  static_assert(kBlocks % 2 == 0, "a wave's dimensions are whole groups of columns");
+  constexpr int kShare = kWavesA / kGroups;      // waves that share out a head group's dimensions
+  constexpr int kBlocks = L / 16 / kShare;       // blocks of 16 dimensions of a wave
+  constexpr int kQueryTiles = (kGroups + 1) / 2; // the queries, as tiles of 32 heads
   extern __shared__ __align__(1024) char smem[];
   char* raw = smem + (kMx ? 2 * S::kTileBytes : 0);  // tiles as loaded (bf16: the tiles themselves)
-  constexpr int kLoadBytes = kMx ? S::kRawBytes : S::kTileBytes;
-  int* list = (int*)(raw + kDepth * kLoadBytes);     // row indices of the part, -1: none
-  const uint32_t raw0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(HS_LDS char*)raw);
+  int* list = (int*)(raw + kDepth * S::kLoadBytes);  // row indices of the part, -1: none
+  const uint32_t smem0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(HS_LDS char*)smem);
+  const uint32_t raw0 = smem0 + (uint32_t)(raw - smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 31, half = lane >> 5;
+  const int col = lane & 15, group = lane >> 4;
   const Part part = part_of(a);
-  const int head = part.h0 + (wave / kShare) * 32 + col;
+  const int head = part.h0 + (wave / kShare) * 16 + col;
   const int share = wave % kShare;
   const int rb = a.row.bytes;
   const int32_t* out = a.out + (size_t)part.r * a.k;
@@ -131,124 +179,169 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
   const uintptr_t far = (uintptr_t)a.tail + ((size_t)part.r * a.T - (size_t)a.B) * rb;
   const uintptr_t none = (uintptr_t)zero_row;
 
-  // the queries, one k-step of 16 values to a register quadruple
-  bf8 q[S::kSteps];
-  const uint32_t sign = a.scale < 0.0f ? kSigns : 0u;
-  {
-    const int h = head < a.heads ? head : a.heads - 1;  // columns behind the last head repeat it, and are dropped
-    const __bf16* src = (const __bf16*)a.q + ((size_t)part.r * a.heads + h) * S::D + 8 * half;
-#pragma unroll
-    for (int s = 0; s < S::kSteps; ++s) q[s] = turned(*(const v4u*)(src + 16 * s), sign);
-  }
-  f16 o[kBlocks];
-#pragma unroll
-  for (int b = 0; b < kBlocks; ++b) o[b] = f16{};
-  float m = -INFINITY, sum = 0.0f, rsum = 0.0f;  // rsum: of the weights as rounded for the second product
-  const float scale = scale_of(a.scale);
-
-  // LDS places of this lane's reads, but for the tile's start
-  int kat[4], vat[2][2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) kat[i] = col * 128 + (((2 * i + half) ^ swizzle(col)) << 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) vat[i / 2][i % 2] = across_place(lane, i / 2, 8 * (i % 2)) + S::kColBytes * (kBlocks / 2 * share);
-
   const int tiles = (part.end - part.begin + kTile - 1) / kTile;
-  auto write_list = [&](int from) {  // of the rows [from, from + kListed) of the part
-    for (int i = tid; i < kListed; i += kAttendThreads) {
-      const int at = part.begin + from + i;
-      int s = at < part.end ? out[at] : -1;
-      s = s >= 0 && s < a.B + a.T ? (a.gather ? at : s) : -1;
-      list[i] = s;
+  constexpr int kPer = kListed / kAttendThreads;
+  auto read_list = [&](int from, int (&s)[kPer]) {  // indices of the rows from `from` on, of the part
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = part.begin + from + i * kAttendThreads + tid;
+      s[i] = out[at < part.end ? at : part.end - 1];
+    }
+  };
+  auto write_list = [&](int from, const int (&s)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = part.begin + from + i * kAttendThreads + tid;
+      const bool there = at < part.end && s[i] >= 0 && s[i] < a.B + a.T;
+      list[i * kAttendThreads + tid] = there ? (a.gather ? at : s[i]) : -1;
     }
   };
   // asks for tile t (behind the last one: whatever the list holds, so that every tile is the same number of loads) and says
   // which of its rows are there
-  const int mine = 8 * wave + (lane >> 3), place = kMx ? lane & 7 : (lane & 7) ^ swizzle(mine);
-  const int rest_mine = 8 * wave + lane / S::kRawRest, rest_place = lane % S::kRawRest;  // 8-bit rows: of the row's rest
+  const bool odd = wave >= kWavesA / 2;
+  const int mine = 8 * (wave & 3) + (lane >> 3), place = (lane & 7) ^ swizzle16(mine);
+  const int rest_mine = (8 * (wave & 3) + lane / S::kRawRest) & (kTile - 1), rest_place = lane % S::kRawRest;
   auto address = [&](int s) {
     const uintptr_t p = (s < edge ? near : far) + (uint64_t)(uint32_t)s * (uint32_t)rb;
     return (const char*)(s < 0 ? none : p);
   };
-  auto load = [&](int t) {
+  struct Rows { int mine, rest, lane; };  // indices of the rows that this lane loads of a tile, and of row lane % 32
+  auto rows_of = [&](int t) {
     const int* rows = list + t * kTile % kListed;
-    const uint32_t to = raw0 + (t & (kDepth - 1)) * kLoadBytes;
-    const char* row = address(rows[mine]);
-    if constexpr (kMx) {
-      load_groups<false, S::kColBytes>(row + 16 * place, nullptr, to + 1024 * wave,
-                                       std::make_integer_sequence<int, S::kRawCols>());
-      const char* rest = address(rows[rest_mine & (kTile - 1)]) + 128 * S::kRawCols + 16 * rest_place;
-      if (lane < 8 * S::kRawRest) load_to_lds<0>(rest, to + S::kRawCols * S::kColBytes + 128 * S::kRawRest * wave);
-    } else {
-      load_groups<S::D % 64 != 0, S::kColBytes>(row + 16 * place, row + 16 * (place & 3), to + 1024 * wave,
-                                                std::make_integer_sequence<int, S::kCols>());
-    }
-    return (uint32_t)__ballot(rows[col] >= 0);
+    return Rows{rows[mine], kMx ? rows[rest_mine] : 0, rows[lane & (kTile - 1)]};
   };
-  write_list(0);
-  // the queries are here before any load to LDS is on its way: a wait for them later would be one for those too
+  auto load = [&](int t, Rows r) {
+    const uint32_t to = raw0 + (t & (kDepth - 1)) * S::kLoadBytes;
+    const char* row = address(r.mine);
+    if constexpr (kMx) {
+      load_half<S::kRawCols, false, S::kColBytes>(odd, row + 16 * (lane & 7), nullptr, to + 1024 * (wave & 3));
+      if (odd) {
+        const char* rest = address(r.rest) + 128 * S::kRawCols + 16 * rest_place;
+        if (lane < 8 * S::kRawRest)
+          load_to_lds<0>(rest, to + S::kRawCols * S::kColBytes + 128 * S::kRawRest * (wave & 3));
+      }
+    } else {
+      load_half<S::kCols, S::D % 64 != 0, S::kColBytes>(odd, row + 16 * place, row + 16 * (place & 3),
+                                                        to + 1024 * (wave & 3));
+    }
+    return (uint32_t)__ballot(r.lane >= 0);
+  };
+  auto wait_tiles = [&](auto later) {  // all but the last `later` tiles asked for are in LDS, for every wave
+    constexpr int n = decltype(later)::value;
+    if (odd) wait_loads_and_meet<S::kOdd * n>();
+    else wait_loads_and_meet<S::kEven * n>();
+  };
+
+  // LDS places of this lane's reads, but for the tile's start
+  int kat[2], vat[4];
 #pragma unroll
-  for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+v"(q[s]));
-  __syncthreads();
+  for (int i = 0; i < 2; ++i) kat[i] = col * 128 + (((4 * i + group) ^ swizzle16(col)) << 4);
+  {
+    const int row = 4 * group + (col >> 2), x = (lane >> 1) & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vat[i] = row * 128 + (((2 * i + x) ^ swizzle16(row)) << 4) + 8 * (lane & 1);
+  }
+
+  // The queries go through LDS as tiles of 32 heads (their rows are read whole, and once), in the places of the last tiles;
+  // the list of rows is on its way at the same time, and so are then the tiles whose places the queries leave.
+  constexpr int kQueryAt = kMx ? 0 : kDepth - kQueryTiles;  // tile place
+  constexpr int kEarly = kMx ? (kQueryTiles <= 2 ? S::kAhead : 0) : (kQueryAt < S::kAhead ? kQueryAt : S::kAhead);
   uint32_t there[S::kAhead + 1];  // of the tiles asked for, the one in use first
+  bf8 q[S::kSteps];
+  {
+    int s[kPer];
+    read_list(0, s);
 #pragma unroll
-  for (int t = 0; t < S::kAhead; ++t) there[t] = load(t);
+    for (int i = 0; i < kQueryTiles; ++i) {
+      const int h = part.h0 + 32 * i + mine;  // heads behind the last one repeat it, and are dropped
+      const char* row = (const char*)a.q + ((size_t)part.r * a.heads + (h < a.heads ? h : a.heads - 1)) * (2 * S::D);
+      load_half<S::kCols, S::D % 64 != 0, S::kColBytes>(odd, row + 16 * place, row + 16 * (place & 3),
+                                                        smem0 + (kQueryAt + i) * S::kTileBytes + 1024 * (wave & 3));
+    }
+    write_list(0, s);
+    wait_loads_and_meet<0>();
+#pragma unroll
+    for (int t = 0; t < kEarly; ++t) there[t] = load(t, rows_of(t));
+    const char* tile = smem + (kQueryAt + wave / kShare / 2) * S::kTileBytes + wave / kShare % 2 * 2048;
+    const uint32_t sign = a.scale < 0.0f ? kSigns : 0u;
+#pragma unroll
+    for (int i = 0; i < S::kSteps; ++i)
+      q[i] = turned(*(const v4u*)(tile + kat[i & 1] + S::kColBytes * (i >> 1)), sign);
+#pragma unroll
+    for (int i = 0; i < S::kSteps; ++i) asm volatile("" : "+v"(q[i]));  // read, before others write there
+    asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+    for (int t = kEarly; t < S::kAhead; ++t) there[t] = load(t, rows_of(t));
+  }
+  f4 o[kBlocks];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) o[b] = f4{};
+  float m = -INFINITY, sum = 0.0f, rsum = 0.0f;  // rsum: of the weights as rounded for the second product
+  const float scale = scale_of(a.scale);
+  Converter<kMx ? L : 0, kMx ? P : 0> convert;
+  Rows next = rows_of(S::kAhead);
   if constexpr (kMx) {
-    wait_loads_and_meet<S::kLoads * (kDepth - 1)>();
-    convert_tile<L, P>(raw, smem, tid);
+    wait_tiles(std::integral_constant<int, kDepth - 1>());
+    convert.read(raw, tid);
+    convert.write(smem, tid);
   }
 
   for (int t = 0; t < tiles; ++t) {
-    wait_loads_and_meet<S::kLoads * (kDepth - 2)>();  // 8-bit rows: for tile t + 1
-    if ((t + S::kAhead) * kTile % kListed == 0) {     // every wave has asked for all that the list named
-      write_list((t + S::kAhead) * kTile);
+    wait_tiles(std::integral_constant<int, kDepth - 2>());  // (8-bit rows: for tile t + 1)
+    const char* tile = smem + (kMx ? t & 1 : t & (kDepth - 1)) * S::kTileBytes;
+    f4 s[2] = {};
+    constexpr int kSet = kGroups == 8 ? 2 : 4;  // k-steps whose rows are read before the steps before them are multiplied
+    bf8 k[2][kSet][2];
+    auto read_keys = [&](int from) {
+#pragma unroll
+      for (int i = 0; i < kSet; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (from + i < S::kSteps)
+            k[from / kSet & 1][i][b] = *(const bf8*)(tile + kat[i & 1] + S::kColBytes * ((from + i) / 2) + 2048 * b);
+    };
+    read_keys(0);
+    there[S::kAhead] = load(t + S::kAhead, next);  // into the place that every wave has left
+    if ((t + S::kAhead + 1) * kTile % kListed == 0) {  // every wave has read all that the list named
+      int more[kPer];
+      read_list((t + S::kAhead + 1) * kTile, more);
+      write_list((t + S::kAhead + 1) * kTile, more);
       __syncthreads();
     }
-    there[S::kAhead] = load(t + S::kAhead);  // into the place that every wave has left
-    const char* tile = smem + (kMx ? t & 1 : t & (kDepth - 1)) * S::kTileBytes;
-    if constexpr (kMx)
-      convert_tile<L, P>(raw + ((t + 1) & (kDepth - 1)) * S::kRawBytes, smem + ((t + 1) & 1) * S::kTileBytes, tid);
-    // S^T
-    f16 s0{};
-    constexpr int kSet = 4;  // k-steps whose rows are read before the steps before them are multiplied
-    bf8 k[2][kSet];
+    next = rows_of(t + S::kAhead + 1);
+    convert.read(raw + ((t + 1) & (kDepth - 1)) * S::kLoadBytes, tid);
+    // S^T of 32 keys, 16 to a block
 #pragma unroll
-    for (int i = 0; i < kSet; ++i) k[0][i] = *(const bf8*)(tile + kat[i]);
+    for (int j = 0; j < S::kSteps; ++j) {
+      if (j % kSet == 0) read_keys(j + kSet);
 #pragma unroll
-    for (int s = 0; s < S::kSteps; s += kSet) {
-#pragma unroll
-      for (int i = 0; i < kSet; ++i)
-        if (s + kSet + i < S::kSteps)
-          k[(s / kSet + 1) & 1][i] = *(const bf8*)(tile + kat[i] + S::kColBytes * ((s + kSet + i) >> 2));
-#pragma unroll
-      for (int i = 0; i < kSet; ++i)
-        if (s + i < S::kSteps)
-          s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[(s / kSet) & 1][i], q[s + i], s0, 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int b = 0; b < 2; ++b)
+        s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j / kSet & 1][j % kSet][b], q[j], s[b], 0, 0, 0);
+      if (j % kSet == kSet - 1) __builtin_amdgcn_sched_barrier(0);
     }
-    // the values' first blocks are on their way during the softmax, the others two blocks ahead of their product
-    constexpr int kReads = 3;
-    bf8 v[kReads][2];
+    // the values' first blocks are on their way during the softmax, the others some blocks ahead of their product
+    constexpr int kReads = kGroups == 8 ? 4 : 6;
+    bf8 v[kReads];
     auto read_values = [&](int b) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const char* at = tile + S::kColBytes * (b >> 1) + 2048 * j;
-        v[b % kReads][j] = read_across(at + vat[b & 1][0], at + vat[b & 1][1]);
-      }
+      const int d = kBlocks * share + b;  // block of the row; vat is for its place in a group of columns
+      const char* at = tile + S::kColBytes * (d >> 2) + (kBlocks % 4 == 0 ? vat[b & 3] : vat[d & 3]);
+      v[b % kReads] = read_across(at, at + 2048);
     };
-    read_values(0);
-    read_values(1);
-    if (there[0] != 0xffffffffu) {
-      const uint32_t mask = there[0] >> (4 * half);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s0[i] = (mask >> (8 * (i / 4) + i % 4)) & 1 ? s0[i] : -INFINITY;
+    for (int b = 0; b < kReads - 1; ++b)
+      if (b < kBlocks) read_values(b);
+    convert.write(smem + ((t + 1) & 1) * S::kTileBytes, tid);
+    if (there[0] != 0xffffffffu) {
+      const uint32_t mask = there[0] >> (4 * group);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i / 4][i % 4] = (mask >> (16 * (i / 4) + i % 4)) & 1 ? s[i / 4][i % 4] : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < S::kAhead; ++i) there[i] = there[i + 1];
-    float top = s0[0];
+    float top = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s0[i]);
-    top = max_of_halves(top) * scale;
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i / 4][i % 4]);
+    top = max_of_quarters(top) * scale;
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top);
       if (__any(m > -INFINITY)) {
@@ -261,85 +354,105 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_kernel(AttendArgs a)
       m = to;
     }
     const float m0 = m == -INFINITY ? 0.0f : m;
-    bf8 p[2];
-    weigh(s0, scale, m0, p, sum, rsum);
+    bf8 p;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) weigh_pair(s[i / 4][i % 4], s[i / 4][i % 4 + 1], scale, m0, p, i, sum, rsum);
     __builtin_amdgcn_sched_barrier(0);
     // O^T
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-      if (b + 2 < kBlocks) read_values(b + 2);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[b % kReads][j], p[j], o[b], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+      if (b + kReads - 1 < kBlocks) read_values(b + kReads - 1);
+      o[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[b % kReads], p, o[b], 0, 0, 0);
+      if (b % 2 == 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads behind the last tile write to LDS too
+  sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
+  rsum += __shfl_xor(rsum, 16);
   rsum += __shfl_xor(rsum, 32);
   if (head >= a.heads) return;
   const size_t rh = (size_t)part.r * a.heads + head;
+  const int first = 16 * kBlocks * share + 4 * group;  // of the lane's dimensions: 4 of every 16
   if (a.splits == 1) {
     const float f = rsum > 0.0f ? 1.0f / rsum : rsum == 0.0f ? 0.0f : rsum;
-    __bf16* dst = (__bf16*)a.o + rh * L + 32 * kBlocks * share + 4 * half;
+    __bf16* dst = (__bf16*)a.o + rh * L + first;
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
+    for (int b = 0; b < kBlocks; ++b) {
+      bf4 v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bf4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (__bf16)(o[b][4 * i + j] * f);
-        *(bf4*)(dst + 32 * b + 8 * i) = v;
-      }
-    if (a.lse && share == 0 && half == 0) a.lse[rh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
+      for (int j = 0; j < 4; ++j) v[j] = (__bf16)(o[b][j] * f);
+      *(bf4*)(dst + 16 * b) = v;
+    }
+    if (a.lse && share == 0 && group == 0)
+      a.lse[rh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
     return;
   }
   // partial results: [R][heads][splits] of (m, sum, rsum, -) and [R][heads][splits][L]
   const size_t ph = rh * a.splits + part.split;
   const size_t stats = (size_t)a.R * a.heads * a.splits * 4;
-  if (share == 0 && half == 0) *(f4*)(a.work + ph * 4) = f4{m, sum, rsum, 0.0f};
-  float* dst = a.work + stats + ph * L + 32 * kBlocks * share + 4 * half;
+  if (share == 0 && group == 0) *(f4*)(a.work + ph * 4) = f4{m, sum, rsum, 0.0f};
+  float* dst = a.work + stats + ph * L + first;
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *(f4*)(dst + 32 * b + 8 * i) = f4{o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]};
+  for (int b = 0; b < kBlocks; ++b) *(f4*)(dst + 16 * b) = o[b];
 }
 
-// Joins the parts of one request and head, in their order: one wave per head, eight (four) dimensions a lane.
+// Joins the parts of one request and head: a workgroup of four waves takes both, each wave every fourth part (all of a wave's
+// parts on their way at once), and the waves' sums are added in their order.
 template <int L>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
-  constexpr int kPer = L / 64;
-  const size_t rh = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (rh >= (size_t)a.R * a.heads) return;
-  const f4* st = (const f4*)a.work + rh * a.splits;
-  float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, st[s][0]);
-  const float m0 = m == -INFINITY ? 0.0f : m;
-  float sum = 0.0f, rsum = 0.0f, o[kPer] = {};
-  const float* src = a.work + (size_t)a.R * a.heads * a.splits * 4 + rh * a.splits * L + lane * kPer;
-  for (int s = 0; s < a.splits; ++s) {
-    const f4 v = st[s];
-    const float c = __builtin_amdgcn_exp2f(v[0] - m0);
-    sum += c * v[1];
-    rsum += c * v[2];
+  constexpr int kPer = L / 64, kOnWay = 4;
+  __shared__ f4 sums[4][L / 4];
+  const size_t rh = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, splits = a.splits;
+  // every lane has one part's figures (there are at most 64 parts)
+  f4 v = {-INFINITY, 0.0f, 0.0f, 0.0f};
+  if (lane < splits) v = ((const f4*)a.work)[rh * splits + lane];
+  const float* src = a.work + (size_t)a.R * a.heads * splits * 4 + rh * splits * L + lane * 4;
+  f4 x[kOnWay][kPer / 4], o[kPer / 4] = {};
+  auto read = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < kPer; i += 4) {
-      const f4 x = *(const f4*)(src + (size_t)s * L + i);
+    for (int i = 0; i < kOnWay; ++i) {
+      const int s = s0 + 4 * i;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i + j] += c * x[j];
+      for (int j = 0; j < kPer / 4; ++j) x[i][j] = *(const f4*)(src + (size_t)(s < splits ? s : 0) * L + 256 * j);
+    }
+  };
+  read(wave);
+  float m = max_of_quarters(v[0]);
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float c = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(v[0] - m);
+  float sum = c * v[1], rsum = c * v[2];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    sum += __shfl_xor(sum, d);
+    rsum += __shfl_xor(rsum, d);
+  }
+  for (int s0 = wave; s0 < splits; s0 += 4 * kOnWay) {
+    if (s0 != wave) read(s0);
+#pragma unroll
+    for (int i = 0; i < kOnWay; ++i) {
+      const int s = s0 + 4 * i;
+      const float w = __shfl(c, s < splits ? s : 0);
+      if (s < splits)
+#pragma unroll
+        for (int j = 0; j < kPer / 4; ++j) o[j] += w * x[i][j];
     }
   }
-  const float f = rsum > 0.0f ? 1.0f / rsum : rsum == 0.0f ? 0.0f : rsum;
-  __bf16* dst = (__bf16*)a.o + rh * L + lane * kPer;
 #pragma unroll
-  for (int i = 0; i < kPer; i += 4) {
-    bf4 v;
+  for (int j = 0; j < kPer / 4; ++j) sums[wave][lane + 64 * j] = o[j];
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d < L / 4) {
+    const f4 all = ((sums[0][d] + sums[1][d]) + sums[2][d]) + sums[3][d];
+    const float f = rsum > 0.0f ? 1.0f / rsum : rsum == 0.0f ? 0.0f : rsum;
+    bf4 r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = (__bf16)(o[i + j] * f);
-    *(bf4*)(dst + i) = v;
+    for (int i = 0; i < 4; ++i) r[i] = (__bf16)(all[i] * f);
+    *(bf4*)((__bf16*)a.o + rh * L + 4 * d) = r;
   }
-  if (a.lse && lane == 0) a.lse[rh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
+  if (a.lse && threadIdx.x == 0) a.lse[rh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
 }
 
 template <int L, int P, bool kMx, int kGroups>
@@ -351,18 +464,19 @@ void launch(const AttendArgs& a, hipStream_t s) {
 
 template <int L, int P, bool kMx>
 hipError_t launch_heads(const AttendArgs& a, hipStream_t s) {
-  if (a.heads <= 32) launch<L, P, kMx, 1>(a, s);
-  else if (a.heads <= 64) launch<L, P, kMx, 2>(a, s);
-  else launch<L, P, kMx, 4>(a, s);
+  if (a.heads <= 16) launch<L, P, kMx, 1>(a, s);
+  else if (a.heads <= 32) launch<L, P, kMx, 2>(a, s);
+  else if (a.heads <= 64) launch<L, P, kMx, 4>(a, s);
+  else launch<L, P, kMx, 8>(a, s);
   if (a.splits > 1)
-    hipLaunchKernelGGL(join_kernel<L>, dim3((int)(((size_t)a.R * a.heads + 3) / 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(join_kernel<L>, dim3(a.R * a.heads), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <int L, int P, bool kMx>
 hipError_t set_lds() {
   for (const void* f : {(const void*)attend_kernel<L, P, kMx, 1>, (const void*)attend_kernel<L, P, kMx, 2>,
-                        (const void*)attend_kernel<L, P, kMx, 4>}) {
+                        (const void*)attend_kernel<L, P, kMx, 4>, (const void*)attend_kernel<L, P, kMx, 8>}) {
     const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<L, P, kMx>::kLds);
     if (e != hipSuccess) return e;
   }
@@ -371,13 +485,26 @@ hipError_t set_lds() {
 
 }  // namespace
 
-int attend_splits(int R, int k, int heads, const RowLayout&) {
-  const int groups = (heads + kGroupHeads - 1) / kGroupHeads;
+// Parts of each selection: the number for which a model of the call's time, in tenths of a microsecond, is least. A
+// workgroup takes 6 us to begin and end and 1.8 us a tile when all 256 compute units stream rows; the join takes 4 us and
+// the time that the partial results take to memory and back (at 5 TB/s). Measured against it, in us: 64 requests x 2048
+// rows x 64 heads in 3, 4, 6, 8 parts 60 (modelled) / 55, 78, 73; 32 x 2048 x 16 in 6, 8, 12 parts 24, 23, 31; 7 x 999 x 20
+// in 8, 16, 32 parts 11, 10, 10.
+int attend_splits(int R, int k, int heads, const RowLayout& row) {
+  const int64_t units = (int64_t)R * ((heads + kGroupHeads - 1) / kGroupHeads);
   const int tiles = (k + kTile - 1) / kTile;
-  int s = 256 / (R * groups);
-  if (s < 1) s = 1;
-  if (s > tiles) s = tiles;
-  return s;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= tiles && s <= kMostSplits; ++s) {
+    const int64_t rounds = (units * s + 255) / 256, per = (tiles + s - 1) / s;
+    int64_t t = rounds * (per * 18 + 60);
+    if (s > 1) t += 40 + (int64_t)R * heads * s * row.latent * 8 / 500000;
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
 }
 
 uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row) {

@@ -53,28 +53,30 @@ __device__ __forceinline__ bf8 turned(v4u x, uint32_t sign) {
 // The magnitude of the scale, to base 2. Not zero: a score that a mask took out, -infinity, stays so.
 __device__ __forceinline__ float scale_of(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1.17549435e-38f); }
 
-// The weights 2^(s scale - m) of two of a lane's scores (i and i + 1 of 16), rounded to bf16 in p for the second product;
-// their sum is added to `sum`, that of the rounded ones, one dot product with ones, to `rsum`.
-__device__ __forceinline__ void weigh_pair(const f16& s, int i, float scale, float m, bf8 p[2], float& sum, float& rsum) {
+// The weights 2^(s scale - m) of two of a lane's scores, rounded to bf16 in p[i] and p[i + 1] for the second product; their
+// sum is added to `sum`, that of the rounded ones, one dot product with ones, to `rsum`.
+__device__ __forceinline__ void weigh_pair(float s0, float s1, float scale, float m, bf8& p, int i, float& sum,
+                                           float& rsum) {
   const bf2 ones = {(__bf16)1.0f, (__bf16)1.0f};
-  const float a = __builtin_amdgcn_exp2f(fmaf(s[i], scale, -m)), b = __builtin_amdgcn_exp2f(fmaf(s[i + 1], scale, -m));
+  const float a = __builtin_amdgcn_exp2f(fmaf(s0, scale, -m)), b = __builtin_amdgcn_exp2f(fmaf(s1, scale, -m));
   const bf2 r = {(__bf16)a, (__bf16)b};
   sum += a;
   sum += b;
   rsum = __builtin_amdgcn_fdot2_f32_bf16(r, ones, rsum, false);
-  p[i / 8][i % 8] = r[0];
-  p[i / 8][i % 8 + 1] = r[1];
-}
-
-__device__ __forceinline__ void weigh(const f16& s, float scale, float m, bf8 p[2], float& sum, float& rsum) {
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) weigh_pair(s, i, scale, m, p, sum, rsum);
+  p[i] = r[0];
+  p[i + 1] = r[1];
 }
 
 // The larger of a lane's value and that of the lane 32 away.
 __device__ __forceinline__ float max_of_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The largest of the values of the four lanes 16 apart.
+__device__ __forceinline__ float max_of_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return max_of_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
 
 // The matrix unit's first operand read across a tile's rows: lane (column d = lane % 32 of the 32 that `lo` begins) gets rows

@@ -269,7 +269,8 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
           for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(m0[g]));
 #pragma unroll
           for (int e = from; e < to; ++e)
-            weigh_pair(x[e / 8], e % 8 * 2, scale, m0[e / 8], p[e / 8], sum[e / 8], rsum[e / 8]);
+            weigh_pair(x[e / 8][e % 8 * 2], x[e / 8][e % 8 * 2 + 1], scale, m0[e / 8], p[e / 8][e % 8 / 4], e % 4 * 2,
+                       sum[e / 8], rsum[e / 8]);
 #pragma unroll
           for (int g = 0; g < kSets; ++g) asm volatile("" : "+v"(sum[g]), "+v"(rsum[g]));
           __builtin_amdgcn_sched_barrier(0);
@@ -291,7 +292,9 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
         read_values(0);
         read_values(1);
 #pragma unroll
-        for (int g = 0; g < kSets; ++g) weigh(x[g], scale, m0[g], p[g], sum[g], rsum[g]);
+        for (int e = 0; e < 8 * kSets; ++e)
+          weigh_pair(x[e / 8][e % 8 * 2], x[e / 8][e % 8 * 2 + 1], scale, m0[e / 8], p[e / 8][e % 8 / 4], e % 4 * 2,
+                     sum[e / 8], rsum[e / 8]);
       }
       bool up = false;
 #pragma unroll
