@@ -29,15 +29,17 @@ struct MaxOp {
   __device__ int operator()(int a, int b) const { return a > b ? a : b; }
 };
 
-// Exclusive scan of one value per thread (0 the neutral element), and the total of all.
+// Exclusive scan of one value per thread (0 the neutral element), and the total of all. Inside a wave by lane shifts: 1, 2,
+// 4, 8 in each row of 16, then lane 15 into the rows 1 and 3, lane 31 into the rows 2 and 3.
 template <class Op>
 __device__ __forceinline__ int map_scan(int v, Op op, int* sh, int lane, int wave, int* total) {
   int x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x = op(y, x);
-  }
+  x = op(__builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false), x);
+  x = op(__builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false), x);
+  x = op(__builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false), x);
+  x = op(__builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false), x);
+  x = op(__builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false), x);
+  x = op(__builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false), x);
   if (lane == 63) sh[wave] = x;
   __syncthreads();
   int before = 0, all = 0;
@@ -48,7 +50,7 @@ __device__ __forceinline__ int map_scan(int v, Op op, int* sh, int lane, int wav
     all = op(all, t);
   }
   __syncthreads();  // sh is free again
-  const int e = __shfl_up(x, 1);
+  const int e = __builtin_amdgcn_update_dpp(0, x, 0x138, 0xf, 0xf, false);  // of the lane before
   *total = all;
   return lane == 0 ? before : op(before, e);
 }
@@ -63,14 +65,23 @@ __global__ __launch_bounds__(kMapThreads) void map_kernel(MapArgs a) {
 #pragma unroll
   for (int i = 0; i < kMapPer; ++i) owner[tid + i * kMapThreads] = 0;
   __syncthreads();
+  // the requests' own outputs are shared out over the workgroups, as their tokens are
+  const int share = (int)(((uint32_t)a.R + gridDim.x - 1) / gridDim.x);
+  const int64_t own0 = (int64_t)blockIdx.x * share, own1 = own0 + share;
   int base = 0;
   for (int r0 = 0; r0 < a.R; r0 += kMapThreads * kMapPer) {
+    if (base >= lo + kMapTokens && r0 >= own1) break;  // nothing behind is this workgroup's
     int len[kMapPer], raw[kMapPer], sum = 0;
+    int had[kMapPer], window[kMapPer];
+    bool own[kMapPer];
     const SatAdd add{n};
 #pragma unroll
     for (int i = 0; i < kMapPer; ++i) {
       const int r = r0 + tid * kMapPer + i;
       raw[i] = r < a.R ? a.fresh[r] : 0;
+      own[i] = r < a.R && r >= own0 && r < own1;
+      had[i] = own[i] && a.status ? a.len[r] : 0;
+      window[i] = own[i] && a.status && a.T > 0 ? a.tail0[r] : 0;
       const int v = raw[i] < 0 ? 0 : raw[i];
       len[i] = v < n ? v : n;
       sum = add(sum, len[i]);
@@ -87,14 +98,14 @@ __global__ __launch_bounds__(kMapThreads) void map_kernel(MapArgs a) {
           owner[p] = r + 1;
           if (p == 0) first_start = at;
         }
-        if (blockIdx.x == 0) {
+        if (own[i]) {
           a.cu[r] = at;
           if (r == a.R - 1) a.cu[a.R] = end;
           if (a.status) {
             bool bad = raw[i] < 0;
             if (end > at) {
-              const int64_t x0 = a.len[r], x1 = x0 + (end - at) - 1;
-              bad |= x0 < 0 || x1 >= a.H || (a.T > 0 && x1 >= (int64_t)a.tail0[r] + a.T);
+              const int64_t x0 = had[i], x1 = x0 + (end - at) - 1;
+              bad |= x0 < 0 || x1 >= a.H || (a.T > 0 && x1 >= (int64_t)window[i] + a.T);
             }
             a.status[r] = bad ? kStatusBad : 0;
           }
@@ -114,30 +125,42 @@ __global__ __launch_bounds__(kMapThreads) void map_kernel(MapArgs a) {
     mark[i] = best;
   }
   const int before = map_scan(best, MaxOp(), sh, lane, wave, &unused);
+  int req[kMapPer], at[kMapPer], had[kMapPer], window[kMapPer], pos[kMapPer], slot[kMapPer];
+  const int t0 = lo + tid * kMapPer;
 #pragma unroll
   for (int i = 0; i < kMapPer; ++i) {
-    const int t = lo + tid * kMapPer + i;
-    if (t >= n) break;
     const int m = mark[i] ? mark[i] : before;
-    int req = -1, pos = -1, slot = -1;
-    if (m && t < base) {
-      req = owner[m - 1] - 1;
-      const int start = m == 1 ? first_start : lo + m - 1;
-      const int64_t x = (int64_t)a.len[req] + (t - start);
-      bool fine = x >= 0 && x < a.H;
-      if (a.T > 0 && fine) {
-        const int64_t t0 = a.tail0[req];
-        if (x >= t0) {
-          if (x < t0 + a.T) slot = a.B + (int)((uint32_t)x % (uint32_t)a.T);
-          else fine = false;
-        }
-      }
-      if (fine) pos = (int)x;
-    }
-    a.req[t] = req;
-    a.pos[t] = pos;
-    a.slot[t] = slot;
+    const bool there = m && t0 + i < base;
+    req[i] = there ? owner[m - 1] - 1 : -1;
+    at[i] = t0 + i - (m == 1 ? first_start : lo + m - 1);
+    had[i] = there ? a.len[req[i]] : 0;
+    window[i] = there && a.T > 0 ? a.tail0[req[i]] : 0;
   }
+#pragma unroll
+  for (int i = 0; i < kMapPer; ++i) {
+    const int64_t x = (int64_t)had[i] + at[i];
+    bool fine = req[i] >= 0 && x >= 0 && x < a.H;
+    slot[i] = -1;
+    if (a.T > 0 && x >= window[i]) {
+      if (x < (int64_t)window[i] + a.T) slot[i] = a.B + (int)((uint32_t)x % (uint32_t)a.T);
+      else fine = false;
+    }
+    pos[i] = fine ? (int)x : -1;
+    slot[i] = fine ? slot[i] : -1;
+  }
+  if (t0 + kMapPer <= n && (((uintptr_t)a.req | (uintptr_t)a.pos | (uintptr_t)a.slot) & 15) == 0) {
+    *(int4*)(a.req + t0) = int4{req[0], req[1], req[2], req[3]};
+    *(int4*)(a.pos + t0) = int4{pos[0], pos[1], pos[2], pos[3]};
+    *(int4*)(a.slot + t0) = int4{slot[0], slot[1], slot[2], slot[3]};
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kMapPer; ++i)
+    if (t0 + i < n) {
+      a.req[t0 + i] = req[i];
+      a.pos[t0 + i] = pos[i];
+      a.slot[t0 + i] = slot[i];
+    }
 }
 
 // ---- store ----
@@ -159,8 +182,22 @@ __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int L = a.row.latent, P = a.row.rope / 2;
   const bool has = lane * 8 < L, pair = lane < P;
+  const int i0 = a.halves ? lane : 2 * lane, i1 = a.halves ? lane + P : 2 * lane + 1;  // of the lane's pair
+  bf8 w{};
+  if (has) w = *(const bf8*)(a.weight + lane * 8);
+  const double freq = pair && a.freqs ? a.freqs[lane] * 0.15915494309189535 : 0.0;  // turns per position
   const int64_t stride = (int64_t)gridDim.x * kStoreWaves;
   for (int64_t t = (int64_t)blockIdx.x * kStoreWaves + wave; t < a.n; t += stride) {
+    // the input is on its way with what says where it goes
+    const uint16_t* in = a.x + t * a.x_stride;
+    bf8 v{};
+    if (has) v = *(const bf8*)(in + lane * 8);
+    __bf16 z0{}, z1{};
+    if (pair) {
+      const __bf16* xr = (const __bf16*)(in + L);
+      z0 = xr[i0];
+      z1 = xr[i1];
+    }
     const int r = a.req[t], x = a.pos[t], slot = a.slot[t];
     if (r < 0 || x < 0 || r >= a.R) continue;
     const int ring = slot - a.B;
@@ -168,12 +205,6 @@ __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
     if (x >= a.H || !(in_tail || slot == -1)) {
       if (a.status && lane == 0) a.status[r] = kStatusBad;
       continue;
-    }
-    const uint16_t* in = a.x + t * a.x_stride;
-    bf8 v{}, w{};
-    if (has) {
-      v = *(const bf8*)(in + lane * 8);
-      w = *(const bf8*)(a.weight + lane * 8);
     }
     float y[8], sq = 0.0f;
 #pragma unroll
@@ -198,15 +229,10 @@ __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
       yb[i] = (__bf16)y[i];
     }
     // the rope part: lane i has pair i
-    const int i0 = a.halves ? lane : 2 * lane, i1 = a.halves ? lane + P : 2 * lane + 1;
-    __bf16 z0{}, z1{};
     if (pair) {
-      const __bf16* xr = (const __bf16*)(in + L);
-      z0 = xr[i0];
-      z1 = xr[i1];
       if (a.freqs) {
         // the angle in turns, in 64 bits, less its whole turns: what is left of it is exact enough in 32
-        const double turns = (double)x * (a.freqs[lane] * 0.15915494309189535);
+        const double turns = (double)x * freq;
         float s, c;
         sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
         const float u = (float)z0, q = (float)z1;
