@@ -900,7 +900,10 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
   a.q = (const uint16_t*)d_q;
   a.kv = (const uint16_t*)d_kv;
   a.krope = (const uint16_t*)d_rope;
-  a.splits = hs::prompt_splits(a.R, n_q, n_k, heads, value);
+  const hs::PromptPlan plan = hs::prompt_plan(a.R, n_q, n_k, heads, value);
+  a.sets = plan.sets;
+  a.splits = plan.splits;
+  a.items = plan.items;
   a.work = (float*)d_work;
   a.cu_q = d_cu_q;
   a.cu_k = d_cu_k;

@@ -88,7 +88,9 @@ struct PromptArgs {
   const int32_t* cu_k;    // [R + 1]
   uint16_t* o;            // [n_q][heads][value]
   float* lse;             // [n_q][heads] or nullptr
-  int32_t splits;         // parts of the keys, each a workgroup's
+  int32_t sets;           // 128 queries to a workgroup each
+  int32_t splits;         // most parts of a query tile's keys
+  int32_t items;          // where splits > 1: parts of all tiles to aim at, for a head
   float* work;            // partial results where splits > 1
 };
 
@@ -96,8 +98,11 @@ struct PromptArgs {
 int attend_splits(int R, int k, int heads, const RowLayout& row);
 uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row);
 
-// The same for hs_attend_prompt: parts of every query tile's keys.
-int prompt_splits(int R, int n_q, int n_k, int heads, int value);
+// The same for hs_attend_prompt.
+struct PromptPlan {
+  int sets, splits, items;
+};
+PromptPlan prompt_plan(int R, int n_q, int n_k, int heads, int value);
 uint64_t prompt_work_bytes(int R, int n_q, int n_k, int heads, int value);
 
 // Allows the attention kernels the LDS that they take, on the current device.

@@ -3,22 +3,26 @@
 //
 //   s = scale * q . key,   o = sum_j p_j value_j / sum_j p_j,   p_j = 2^(s_j log2 e - m)   (m a running maximum)
 //
-// One pass over the keys. A workgroup of four waves takes 256 (128) queries of one sequence and head, 64 (32) to a wave.
+// One pass over the keys. A workgroup of four waves takes 256 or 128 queries of one sequence and head, 64 or 32 to a wave.
 // Matrix instructions do both products transposed, so that a query is a lane's column in both and its maximum, sum and
 // rescaling stay inside the lane:
 //   S^T[key][query]  = K Q^T     A: keys from LDS, B: the queries, kept in registers
 //   O^T[dim][query] += V^T P^T   A: values read through the transposing LDS load, B: the weights as S^T left them
 // (a lane half h holds the keys 8 i + 4 h + 0..3 of S^T; the second product takes its keys in that order).
-// There is one wave to a SIMD, so the two pipes are kept busy from within it: a step of 32 keys computes the next step's
+// There are only one or two waves to a SIMD, so the two pipes are kept busy from within it: a step of 32 keys computes the next step's
 // scores between the exponentials of its own, and takes their maximum between its products with the values.
 #include "hs_latent.h"
 #include "hs_mfma.h"
+
+#include <math.h>
 
 #include <utility>
 
 namespace hs {
 
 namespace {
+
+constexpr int kLeastKeys = 512;  // keys of a part of a sequence: below, the parts' own costs are more than they save
 
 __device__ __align__(16) uint4 zero_key[64];  // what a tile holds behind the last key
 
@@ -27,9 +31,9 @@ template <int DN, int P, int DV, int kSets>
 struct PromptShape {
   static constexpr int kWaves = 4;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kPer = DV == 256 ? 1 : 2;      // steps of 32 keys to a tile
+  static constexpr int kPer = DV == 64 || kSets == 2 ? 2 : 1;  // steps of 32 keys to a tile
   static constexpr int kKeys = 32 * kPer;
-  static constexpr int kDepth = kPer == 2 ? 3 : 4;    // tiles in LDS: one or two in use, the others on their way
+  static constexpr int kDepth = DV == 256 ? 4 : 3;    // tiles in LDS: one or two in use, the others on their way
   static constexpr int kQueries = 32 * kSets * kWaves;
   static constexpr int kSteps = (DN + P) / 16;
   static constexpr int kKeyCols = DN / 64 + 1, kValueCols = DV / 64;  // groups of 64 columns (the last key group: rope)
@@ -51,18 +55,82 @@ __device__ __forceinline__ void wait_tile(int later) {
 
 __device__ __forceinline__ int cut(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
-// The sequence of query tile `id` and the tile's number in it: a scan over the sequences' tile counts, one to a thread.
+// Sums of kN values over the workgroup, in the same order in every workgroup. sh: kN * kWaves values.
+template <int kN, int kWaves>
+__device__ __forceinline__ void block_sums(float (&x)[kN], float* sh) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x[i] += __shfl_xor(x[i], d);
+    if ((threadIdx.x & 63) == 0) sh[i * kWaves + (threadIdx.x >> 6)] = x[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    x[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) x[i] += sh[i * kWaves + w];
+  }
+  __syncthreads();
+}
+
+struct Item {  // a workgroup's share: part `part` of the keys of query tile `tile` of a sequence
+  int tile, part, parts;
+  int q0, nq, k0, nk;  // of the sequence: its first query and key, and how many of both
+};
+
+// Item `id` of a head: the sequences from the last to the first, each one's tiles from the last (it sees the most keys) to
+// the first, each tile's parts. A sequence's keys are cut into as many parts as makes about a.items of equal length of all
+// sequences' tiles, at most a.splits: the finest of four lengths that makes no more (one more would wait for a round of
+// its own; 4 chunks of 512 tokens behind 4K to 16K x 8 heads x 256 values 274 -> 227 us against equal counts of parts).
+// A scan over the sequences' item counts, one to a thread.
 template <int kQueries, int kWaves>
-__device__ __forceinline__ bool find_tile(const PromptArgs& a, int id, int* seq, int* tile, int* sh) {
+__device__ __forceinline__ bool find_item(const PromptArgs& a, int id, Item* it, int* sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int before = 0;
-  for (int r0 = 0; r0 < a.R; r0 += 64 * kWaves) {
-    const int r = r0 + tid;
-    int c = 0;
-    if (r < a.R) {
-      const int n = cut(a.cu_q[r + 1], a.n_q) - cut(a.cu_q[r], a.n_q);
-      c = n > 0 ? (n + kQueries - 1) / kQueries : 0;
+  struct Sequence {
+    int q0, nq, k0, nk, tiles;
+  };
+  auto sequence = [&](int r) {
+    Sequence q{};
+    if (r >= 0) {
+      const int q1 = a.cu_q[r + 1], k1 = a.cu_k[r + 1];
+      q.q0 = cut(a.cu_q[r], a.n_q);
+      q.k0 = cut(a.cu_k[r], a.n_k);
+      q.nq = cut(q1, a.n_q) - q.q0;
+      q.nk = cut(k1, a.n_k) - q.k0;
+      q.nk = q.nk > 0 ? q.nk : 0;
+      q.tiles = q.nq > 0 ? (q.nq + kQueries - 1) / kQueries : 0;
     }
+    return q;
+  };
+  float per = 0.0f;  // parts to a key
+  auto parts_of = [&](int keys, float per) {
+    const int parts = (int)((float)keys * fminf(per, 1.0f / kLeastKeys) + 0.5f);
+    return parts < 1 ? 1 : parts > a.splits ? a.splits : parts;
+  };
+  if (a.splits > 1) {
+    float all[1] = {};
+    for (int r = a.R - 1 - tid; r >= 0; r -= 64 * kWaves) {
+      const Sequence q = sequence(r);
+      all[0] += (float)q.tiles * (float)q.nk;
+    }
+    block_sums<1, kWaves>(all, (float*)sh);
+    per = (float)a.items / fmaxf(all[0], 1.0f);
+    float count[4] = {};
+    for (int r = a.R - 1 - tid; r >= 0; r -= 64 * kWaves) {
+      const Sequence q = sequence(r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) count[i] += (float)q.tiles * (float)parts_of(q.nk, per * (1.1f - 0.1f * i));
+    }
+    block_sums<4, kWaves>(count, (float*)sh);
+    const float most = (float)a.items;
+    per *= count[0] <= most ? 1.1f : count[1] <= most ? 1.0f : count[2] <= most ? 0.9f : 0.8f;
+  }
+  int before = 0;
+  for (int r0 = a.R - 1; r0 >= 0; r0 -= 64 * kWaves) {
+    const Sequence q = sequence(r0 - tid);
+    const int parts = a.splits > 1 ? parts_of(q.nk, per) : 1;
+    const int c = q.tiles * parts;
     int x = c;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -70,7 +138,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int id, int* seq,
       if (lane >= d) x += y;
     }
     if (lane == 63) sh[wave] = x;
-    if (tid == 0) sh[kWaves] = -1;
+    if (tid == 0) sh[kWaves] = 0;
     __syncthreads();
     int total = 0;
     for (int w = 0; w < kWaves; ++w) {
@@ -78,15 +146,17 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int id, int* seq,
       total += sh[w];
     }
     if (id >= before + x - c && id < before + x) {
-      sh[kWaves] = r;
-      sh[kWaves + 1] = id - (before + x - c);
+      const int at = id - (before + x - c);
+      const int v[7] = {parts, q.tiles - 1 - at / parts, at % parts, q.q0, q.nq, q.k0, q.nk};
+      for (int i = 0; i < 7; ++i) sh[kWaves + i] = v[i];
     }
     __syncthreads();
-    const int found = sh[kWaves], at = sh[kWaves + 1];
+    int v[7];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) v[i] = __builtin_amdgcn_readfirstlane(sh[kWaves + i]);
     __syncthreads();
-    if (found >= 0) {
-      *seq = __builtin_amdgcn_readfirstlane(found);
-      *tile = __builtin_amdgcn_readfirstlane(at);
+    if (v[0] > 0) {
+      *it = Item{v[1], v[2], v[0], v[3], v[4], v[5], v[6]};
       return true;
     }
     before += total;
@@ -105,11 +175,12 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
   constexpr int kWaves = S::kWaves;
   constexpr int kBlocks = DV / 32;
   extern __shared__ __align__(1024) char smem[];
-  __shared__ int sh[kWaves + 2];
+  __shared__ int sh[4 * kWaves];
+  static_assert(4 * kWaves >= kWaves + 7);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(HS_LDS char*)smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const int h = blockIdx.x % a.heads, split = blockIdx.x / a.heads;
+  const int h = blockIdx.x;
   int kat[4], vat[2][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) kat[i] = col * 128 + (((2 * i + half) ^ swizzle(col)) << 4);
@@ -119,19 +190,15 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
   const uint32_t sign = a.scale < 0.0f ? kSigns : 0u;
 
   for (int slot = blockIdx.y; slot < slots; slot += gridDim.y) {
-    // the last tiles of a sequence see the most keys, and go first
-    int seq, qt;
-    if (!find_tile<S::kQueries, kWaves>(a, slots - 1 - slot, &seq, &qt, sh)) continue;
-    const int q0 = cut(a.cu_q[seq], a.n_q), nq = cut(a.cu_q[seq + 1], a.n_q) - q0;
-    const int k0 = cut(a.cu_k[seq], a.n_k);
-    int nk = cut(a.cu_k[seq + 1], a.n_k) - k0;
-    if (nk < 0) nk = 0;
-    const int first = qt * S::kQueries;
+    Item it;
+    if (!find_item<S::kQueries, kWaves>(a, slot, &it, sh)) return;
+    const int q0 = it.q0, nq = it.nq, k0 = it.k0, nk = it.nk;
+    const int first = it.tile * S::kQueries;
     // keys that the workgroup's last query sees, and its part of their tiles
     const int last_q = first + S::kQueries < nq ? first + S::kQueries - 1 : nq - 1;
     const int end = a.causal ? cut(nk - nq + last_q + 1, nk) : nk;
     const int all = (end + S::kKeys - 1) / S::kKeys;
-    const int t0 = (int)((int64_t)all * split / a.splits), t1 = (int)((int64_t)all * (split + 1) / a.splits);
+    const int t0 = (int)((int64_t)all * it.part / it.parts), t1 = (int)((int64_t)all * (it.part + 1) / it.parts);
 
     const int wq = first + wave * 32 * kSets;  // the wave's first query
     int limit[kSets];                           // keys that the lane's queries see
@@ -361,7 +428,10 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       const int i = wq + 32 * g + col;
       if (i >= nq) continue;
       const size_t qh = (size_t)(q0 + i) * a.heads + h;
-      if (a.splits == 1) {
+      // (m, sum, rsum, parts) of every query, head and part, and behind them the parts' values
+      const size_t ph = qh * a.splits + it.part;
+      if (a.splits > 1 && half == 0) *(f4*)(a.work + ph * 4) = f4{m[g], sum[g], rsum[g], (float)it.parts};
+      if (it.parts == 1) {
         const float f = rsum[g] > 0.0f ? 1.0f / rsum[g] : rsum[g] == 0.0f ? 0.0f : rsum[g];
         __bf16* dst = (__bf16*)a.o + qh * DV + 4 * half;
 #pragma unroll
@@ -377,9 +447,6 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
           a.lse[qh] = sum[g] > 0.0f ? m[g] * kLn2 + logf(sum[g]) : sum[g] == 0.0f ? -INFINITY : sum[g];
         continue;
       }
-      // partial results: (m, sum, rsum, -) and the values of every query, head and part
-      const size_t ph = qh * a.splits + split;
-      if (half == 0) *(f4*)(a.work + ph * 4) = f4{m[g], sum[g], rsum[g], 0.0f};
       float* dst = a.work + (size_t)a.n_q * a.heads * a.splits * 4 + ph * DV + 4 * half;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
@@ -390,21 +457,25 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
   }
 }
 
-// Joins the parts of each query and head in their order: one wave for both, DV / 64 values a lane.
+// Joins the parts of each query and head in their order: one wave for both, DV / 64 values a lane. What was left in one
+// part has its result.
 template <int DV>
 __global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
   constexpr int kPer = DV / 64;
   const int lane = threadIdx.x & 63;
-  // rows behind the last sequence have no parts
-  const size_t n = (size_t)cut(a.cu_q[a.R], a.n_q) * a.heads;
-  for (size_t qh = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6); qh < n; qh += (size_t)gridDim.x * 4) {
+  // rows before the first sequence and behind the last have no parts
+  const size_t n0 = (size_t)cut(a.cu_q[0], a.n_q) * a.heads, n = (size_t)cut(a.cu_q[a.R], a.n_q) * a.heads;
+  for (size_t qh = n0 + (size_t)blockIdx.x * 4 + (threadIdx.x >> 6); qh < n; qh += (size_t)gridDim.x * 4) {
     const f4* st = (const f4*)a.work + qh * a.splits;
+    const float count = st[0][3];
+    const int parts = count >= 2.0f && count <= (float)a.splits ? (int)count : 1;
+    if (parts == 1) continue;
     float m = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, st[s][0]);
+    for (int s = 0; s < parts; ++s) m = fmaxf(m, st[s][0]);
     const float m0 = m == -INFINITY ? 0.0f : m;
     float sum = 0.0f, rsum = 0.0f, o[kPer] = {};
     const float* src = a.work + (size_t)a.n_q * a.heads * a.splits * 4 + qh * a.splits * DV + lane * kPer;
-    for (int s = 0; s < a.splits; ++s) {
+    for (int s = 0; s < parts; ++s) {
       const f4 v = st[s];
       const float c = __builtin_amdgcn_exp2f(v[0] - m0);
       sum += c * v[1];
@@ -420,16 +491,17 @@ __global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
   }
 }
 
-constexpr int sets_of(int value) { return value == 256 ? 1 : 2; }
+constexpr int queries_of(int sets) { return 128 * sets; }
 
-template <int DN, int P, int DV>
+template <int DN, int P, int DV, int kSets>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
-  constexpr int kSets = sets_of(DV);
   using S = PromptShape<DN, P, DV, kSets>;
+  static_assert(S::kQueries == queries_of(kSets));
   constexpr uint32_t lds = S::kLds;
-  // every sequence but one may leave a tile part empty
-  const int64_t slots = ((int64_t)a.n_q + S::kQueries - 1) / S::kQueries + a.R - 1;
-  hipLaunchKernelGGL((prompt_kernel<DN, P, DV, kSets>), dim3(a.heads * a.splits, (int)(slots < 65535 ? slots : 65535)),
+  // every sequence but one may leave a tile part empty; a tile's parts are at most its share of a.items and one more
+  int64_t slots = ((int64_t)a.n_q + S::kQueries - 1) / S::kQueries + a.R - 1;
+  if (a.splits > 1) slots += a.items + 1;
+  hipLaunchKernelGGL((prompt_kernel<DN, P, DV, kSets>), dim3(a.heads, (int)(slots < 65535 ? slots : 65535)),
                      dim3(S::kThreads), lds, s, a, (int)slots);
   if (a.splits > 1) {
     const uint64_t blocks = ((uint64_t)a.n_q * a.heads + 3) / 4;
@@ -438,33 +510,65 @@ hipError_t launch(const PromptArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DN, int P, int DV>
+template <int DN, int P, int DV, int kSets>
 hipError_t set_lds() {
-  return hipFuncSetAttribute((const void*)prompt_kernel<DN, P, DV, sets_of(DV)>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)PromptShape<DN, P, DV, sets_of(DV)>::kLds);
+  return hipFuncSetAttribute((const void*)prompt_kernel<DN, P, DV, kSets>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)PromptShape<DN, P, DV, kSets>::kLds);
 }
 
 }  // namespace
 
-int prompt_splits(int R, int n_q, int n_k, int heads, int value) {
-  const int queries = value == 256 ? 128 : 256;
-  const int64_t groups = ((int64_t)n_q + queries - 1) / queries * heads;
-  if (groups <= 0) return 1;
-  int64_t s = 256 / groups;
-  const int64_t most = n_k / R / 512;
-  if (s > most) s = most;
-  if (s > 16) s = 16;
-  return s < 1 ? 1 : (int)s;
+// Queries to a workgroup and parts of the keys, by an estimate of the time for sequences of equal lengths under a causal
+// mask. A workgroup's time is its keys' and a start's, the card's that of its longest workgroup or of all of them on 256
+// units, and of a longest one's half where they end unevenly (several sequences, two workgroups to a unit). The join
+// moves the partial results to memory and back.
+// 256 queries to a workgroup (one to a unit) read half as much from LDS for a product as 128 (two to a unit): 8192 tokens x
+// 16 heads with 128 values take 374 and 416 us. But 128 fill the card sooner and hide each other's starts: 8 prompts of up
+// to 300 tokens x 16 heads take 25 and 16 us, 64 of them 93 and 56. With 64 values they are even (32 heads 507 and 482
+// us, 16 heads 258 and 265), and there is one kernel; with 256, the results of 256 queries do not fit into the registers.
+PromptPlan prompt_plan(int R, int n_q, int n_k, int heads, int value) {
+  PromptPlan best{1, 1, 0};
+  if (n_q <= 0) return best;
+  double least = 0.0;
+  const double nq = (double)n_q / R, nk = (double)n_k / R;
+  const double mean = nq < nk ? nk - nq / 2 : nk / 2;  // keys of a query
+  for (int sets = value == 128 ? 2 : 1; sets >= 1; --sets) {
+    const bool two = value == 64 || (value == 128 && sets == 1);  // workgroups to a unit
+    const double per_key = value == 64 ? 0.0147 : value == 256 ? 0.035 : sets == 2 ? 0.0425 : 0.0235;  // us
+    const double tiles = R == 1 ? ceil(nq / queries_of(sets)) : (nq / queries_of(sets) + 0.5) * R, groups = tiles * heads;
+    const double start = 6.0 * sets / per_key;  // keys
+    const int units = two ? 512 : 256;
+    // k = 0: whole; else with one sequence k + 1 parts of each tile, with several k rounds of parts on all units
+    for (int k = 0; k < 16; ++k) {
+      const double most = tiles * fmin(16.0, nk / kLeastKeys);
+      const int items = (int)fmin(R == 1 ? tiles * (k + 1) : (double)k * units / heads, most);
+      const double parts = k == 0 ? 1.0 : items / tiles;
+      if (k > 0 && (parts < 1.25 || groups * parts > 4096)) continue;
+      const double longest = nk / parts + start, each = mean / parts + start, rounds = groups * parts / 256;
+      const double all = R > 1 && k > 0 ? 1.15 * rounds * each
+                         : R == 1 && !two ? ceil(rounds) * each : rounds * each + longest / 4;
+      double t = per_key * (longest > all ? longest : all);
+      if (k > 0) t += 5.0 + (double)n_q * heads * parts * (16 + 4 * value) * 2 / 4.5e6;
+      if (least == 0.0 || t < least) {
+        least = t;
+        best.sets = sets;
+        best.splits = k == 0 ? 1 : R == 1 ? (int)ceil(parts) : parts <= 8 ? (int)ceil(2 * parts) : 16;
+        best.items = k == 0 ? 0 : items;
+      }
+    }
+  }
+  return best;
 }
 
 uint64_t prompt_work_bytes(int R, int n_q, int n_k, int heads, int value) {
-  const uint64_t s = (uint64_t)prompt_splits(R, n_q, n_k, heads, value);
+  const uint64_t s = (uint64_t)prompt_plan(R, n_q, n_k, heads, value).splits;
   return s == 1 ? 0 : (uint64_t)n_q * heads * s * (16 + 4ull * value);
 }
 
 hipError_t set_prompt_lds() {
-  for (const auto f : {set_lds<64, 32, 64>, set_lds<64, 64, 64>, set_lds<128, 32, 128>, set_lds<128, 64, 128>,
-                       set_lds<192, 32, 256>, set_lds<192, 64, 256>}) {
+  for (const auto f : {set_lds<64, 32, 64, 1>, set_lds<64, 64, 64, 1>, set_lds<128, 32, 128, 1>, set_lds<128, 64, 128, 1>,
+                       set_lds<128, 32, 128, 2>, set_lds<128, 64, 128, 2>, set_lds<192, 32, 256, 1>,
+                       set_lds<192, 64, 256, 1>}) {
     const hipError_t e = f();
     if (e != hipSuccess) return e;
   }
@@ -474,9 +578,10 @@ hipError_t set_prompt_lds() {
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t s) {
   if (a.n_q <= 0) return hipSuccess;
   const bool more = a.rope == 64;
-  if (a.value == 64) return more ? launch<64, 64, 64>(a, s) : launch<64, 32, 64>(a, s);
-  if (a.value == 128) return more ? launch<128, 64, 128>(a, s) : launch<128, 32, 128>(a, s);
-  return more ? launch<192, 64, 256>(a, s) : launch<192, 32, 256>(a, s);
+  if (a.value == 64) return more ? launch<64, 64, 64, 1>(a, s) : launch<64, 32, 64, 1>(a, s);
+  if (a.value == 256) return more ? launch<192, 64, 256, 1>(a, s) : launch<192, 32, 256, 1>(a, s);
+  if (a.sets == 2) return more ? launch<128, 64, 128, 2>(a, s) : launch<128, 32, 128, 2>(a, s);
+  return more ? launch<128, 64, 128, 1>(a, s) : launch<128, 32, 128, 1>(a, s);
 }
 
 }  // namespace hs

@@ -422,7 +422,7 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
  *   d_rope  rope values of key token j at d_rope + j * rope_stride elements (16-byte aligned, stride a multiple of 8)
  *   d_cu_q, d_cu_k  [R + 1] starts of each request's queries and keys, ascending from 0 (values are cut to
  *           [0, n_q] and [0, n_k]; a request whose end lies before its start has none; a query row that two requests
-           name gets either's result)
+ *           name has no defined result)
  *   causal  1: query i of a request with m queries and n keys sees its first n - m + i + 1 keys (the queries are the last
  *           m tokens); 0: all n
  *   d_o     [n_q][heads][value] bf16, 16-byte aligned;  d_lse [n_q][heads] float32 or NULL. Zeros and -inf for a query
