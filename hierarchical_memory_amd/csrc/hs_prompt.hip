@@ -22,6 +22,8 @@ namespace hs {
 
 namespace {
 
+typedef unsigned short us8 __attribute__((ext_vector_type(8)));
+
 constexpr int kLeastKeys = 512;  // keys of a part of a sequence: below, the parts' own costs are more than they save
 
 __device__ __align__(16) uint4 zero_key[64];  // what a tile holds behind the last key
@@ -53,6 +55,9 @@ __device__ __forceinline__ void wait_tile(int later) {
   wait_loads_and_meet<0>();
 }
 
+// whether bf16 bits are infinite or NaN
+__device__ __forceinline__ bool is_odd(unsigned short x) { return (x & 0x7f80) == 0x7f80; }
+
 __device__ __forceinline__ int cut(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
 // Sums of kN values over the workgroup, in the same order in every workgroup. sh: kN * kWaves values.
@@ -83,7 +88,7 @@ struct Item {  // a workgroup's share: part `part` of the keys of query tile `ti
 // the first, each tile's parts. A sequence's keys are cut into as many parts as makes about a.items of equal length of all
 // sequences' tiles, at most a.splits: the finest of four lengths that makes no more (one more would wait for a round of
 // its own; 4 chunks of 512 tokens behind 4K to 16K x 8 heads x 256 values 274 -> 227 us against equal counts of parts).
-// A scan over the sequences' item counts, one to a thread.
+// A scan over the sequences' item counts, one to a thread. sh[4 * kWaves] is 0 behind it.
 template <int kQueries, int kWaves>
 __device__ __forceinline__ bool find_item(const PromptArgs& a, int id, Item* it, int* sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -149,6 +154,7 @@ __device__ __forceinline__ bool find_item(const PromptArgs& a, int id, Item* it,
       const int at = id - (before + x - c);
       const int v[7] = {parts, q.tiles - 1 - at / parts, at % parts, q.q0, q.nq, q.k0, q.nk};
       for (int i = 0; i < 7; ++i) sh[kWaves + i] = v[i];
+      sh[4 * kWaves] = 0;
     }
     __syncthreads();
     int v[7];
@@ -175,7 +181,7 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
   constexpr int kWaves = S::kWaves;
   constexpr int kBlocks = DV / 32;
   extern __shared__ __align__(1024) char smem[];
-  __shared__ int sh[4 * kWaves];
+  __shared__ int sh[4 * kWaves + 1];
   static_assert(4 * kWaves >= kWaves + 7);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(HS_LDS char*)smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -250,9 +256,36 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       }
       place_in = place_in + 1 < S::kDepth ? place_in + 1 : 0;
     };
+    // An infinite value or a NaN of a key that some of the workgroup's queries see and others do not would reach those too (a
+    // weight of zero makes it NaN): the lane takes such ones out of its chunks of the tile, and the queries that see them
+    // get them at the end. Only tiles that some query does not see whole are looked through (8192 tokens x 16 heads: no
+    // difference; 8 prompts of up to 300 tokens, where all are, 14.5 -> 15.2 us).
+    const int all_see = a.causal ? cut(nk - nq + first + 1, nk) : nk;  // keys that every query of the workgroup sees
+    auto take_odd = [&](char* at) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      auto chunk = [&](int i) {
+        return (us8*)(at + (S::kKeyCols + i / S::kPer) * S::kColBytes + 4096 * (i % S::kPer) + 1024 * wave + 16 * lane);
+      };
+      us8 most{};
+#pragma unroll
+      for (int i = 0; i < S::kPer * S::kValueCols; ++i)
+        most = __builtin_elementwise_max(most, *chunk(i) & (unsigned short)0x7fff);
+      // 0x7f7f: the largest number; what is above it has another bit
+      const v4u m = (v4u)__builtin_elementwise_max(most, us8{} + (unsigned short)0x7f7f);
+      if ((m[0] | m[1] | m[2] | m[3]) == 0x7f7f7f7fu) return;
+#pragma unroll 1
+      for (int i = 0; i < S::kPer * S::kValueCols; ++i) {
+        us8 x = *chunk(i);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) x[n] = is_odd(x[n]) ? 0 : x[n];
+        *chunk(i) = x;
+      }
+      sh[4 * kWaves] = 1;
+    };
     // tile t is in LDS for every wave; the one that was used before it is left by all, and loaded anew
     const char* tile = smem;
     auto next_tile = [&](int t) {
+      if (S::kKeys * (t + 1) > all_see) take_odd(smem + place_out * S::kTileBytes);
       wait_tile<S::kLoads, S::kDepth - 3>(t1 - 1 - t);
       if (t + S::kDepth - 2 < t1) load(t + S::kDepth - 2);
       tile = smem + place_out * S::kTileBytes;
@@ -308,12 +341,13 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       }
     };
     const int mine_end = (hi + 31) / 32;  // the wave's steps end here; the others' loads and barriers go on
-    // step i with its scores in x; those of step i + 1 go to y
-    auto step = [&](int i, f16 (&x)[kSets], f16 (&y)[kSets]) {
-      const char* values = tile + 4096 * (i % S::kPer);
-      if ((i + 1) % S::kPer == 0 && i + 1 < S::kPer * t1) next_tile((i + 1) / S::kPer);
+    // step i (odd: of a pair's second) with its scores in x; those of step i + 1 go to y
+    auto step = [&](auto odd, int i, f16 (&x)[kSets], f16 (&y)[kSets]) {
+      constexpr int kAt = odd.value % S::kPer, kNext = (odd.value + 1) % S::kPer;  // place in the tile
+      const char* values = tile + 4096 * kAt;
+      if (kNext == 0 && i + 1 < S::kPer * t1) next_tile((i + 1) / S::kPer);
       if (i >= mine_end) return;
-      const char* keys = tile + 4096 * ((i + 1) % S::kPer);
+      const char* keys = tile + 4096 * kNext;
       bf8 p[kSets][2];
       float m0[kSets];
 #pragma unroll
@@ -415,8 +449,8 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
         if (raises()) raise();
       }
       for (int i = begin; i < S::kPer * t1; i += 2) {
-        step(i, s[0], s[1]);
-        if (i + 1 < S::kPer * t1) step(i + 1, s[1], s[0]);
+        step(std::integral_constant<int, 0>(), i, s[0], s[1]);
+        if (i + 1 < S::kPer * t1) step(std::integral_constant<int, 1>(), i + 1, s[1], s[0]);
       }
     }
     asm volatile("s_barrier" ::: "memory");  // every wave has left the tiles
@@ -453,6 +487,28 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *(f4*)(dst + 32 * b + 8 * c) = f4{o[g][b][4 * c], o[g][b][4 * c + 1], o[g][b][4 * c + 2], o[g][b][4 * c + 3]};
+    }
+    if (sh[4 * kWaves]) {
+      // what was taken out, added to what the lane wrote
+      const int from = all_see / S::kKeys > t0 ? all_see / S::kKeys : t0;
+      for (int key = S::kKeys * from; key < S::kKeys * t1 && key < hi; ++key) {
+        const unsigned short* value = (const unsigned short*)a.kv + ((size_t)(k0 + key) * a.heads + h) * (DN + DV) + DN;
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+          const int i = wq + 32 * g + col;
+          if (i >= nq || key >= limit[g]) continue;
+          const size_t qh = (size_t)(q0 + i) * a.heads + h;
+          __bf16* whole = (__bf16*)a.o + qh * DV;
+          float* partial = a.work + (size_t)a.n_q * a.heads * a.splits * 4 + (qh * a.splits + it.part) * DV;
+#pragma unroll 1
+          for (int d = 4 * half; d < DV; d += d % 4 == 3 ? 5 : 1) {
+            if (!is_odd(value[d])) continue;
+            const float x = __uint_as_float((uint32_t)value[d] << 16);
+            if (it.parts == 1) whole[d] = (__bf16)((float)whole[d] + x);
+            else partial[d] += x;
+          }
+        }
+      }
     }
   }
 }

@@ -430,7 +430,7 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
  *   d_work  hs_attend_prompt_work_bytes bytes of device memory, as in hs_attend (few queries over many keys are shared out
  *           over the keys too, and joined)
  * heads: 1 .. 512; (nope, value) one of (64, 64), (128, 128), (192, 256); rope 32 or 64; n_q, n_k from 0 to 2^30.
- * Precision as in hs_attend.
+ * Precision as in hs_attend. An infinite value or a NaN in a key or value row reaches only the queries that see the row.
  */
 int hs_attend_prompt_work_bytes(int32_t num_requests, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope, int32_t rope,
                                 int32_t value, uint64_t* bytes);

@@ -581,6 +581,39 @@ def test_prompt_keys_in_parts(nq, nk, heads, causal, nope, rope, value):
     sw.close()
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("nope,rope,value", DIMS)
+@pytest.mark.parametrize("nq,nk", [([70, 300], [70, 300]), ([5, 40], [300, 77]), ([30], [2600])])
+def test_prompt_values_that_are_no_numbers(nq, nk, nope, rope, value, causal):
+    """An infinite value or a NaN reaches the queries that see its key, in its place, and nothing else."""
+    heads = 2
+    sw, args = _prompt_case(nq, nk, heads, nope, rope, value, causal, seed=value, check=False)
+    q, kv, rows, _, _, scale, o, lse, _ = args
+    keys = []  # (sequence, key of it, head, place, what is there)
+    for r in range(len(nq)):
+        last = nk[r] - 1
+        keys += [(r, last, 0, 1, math.nan), (r, last - 3, 1, value - 1, math.inf), (r, last - nq[r] // 2, 0, 5, -math.inf),
+                 (r, max(last - nq[r] + 2, 0), 1, 37, math.nan)]
+    starts = _cu(nk)
+    clean = kv.cpu().double()
+    for r, key, h, place, what in keys:
+        kv[int(starts[r]) + key, h, nope + place] = what
+        clean[int(starts[r]) + key, h, nope + place] = 0.0
+    hm.hs_attend_prompt(sw.ctx, *args)
+    for r in range(len(nq)):
+        a, b, c, d = int(_cu(nq)[r]), int(_cu(nq)[r + 1]), int(starts[r]), int(starts[r + 1])
+        for h in range(heads):
+            w = ref.prompt(q[a:b, h].cpu().double(), clean[c:d, h], rows[c:d].cpu().double(), nope, scale, causal)
+            got = o[a:b, h].clone()
+            for rr, key, hh, place, _ in keys:
+                if (rr, hh) == (r, h):
+                    first = max(0, key - (nk[r] - nq[r])) if causal else 0
+                    assert not got[first:, place].isfinite().any(), (r, h, key, place)
+                    got[first:, place], w[0][first:, place] = 0.0, 0.0
+            _within(got, w[0], w[2], f"sequence {r} head {h} o")
+            _within(lse[a:b, h], w[1], w[3], f"sequence {r} head {h} lse")
+
+
 def test_prompt_many_sequences():
     n = [(7 * i) % 23 for i in range(700)]
     sw, _ = _prompt_case(n, [m + i % 3 for i, m in enumerate(n)], 2, 64, 32, 64, True, seed=5)
