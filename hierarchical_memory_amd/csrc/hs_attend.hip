@@ -159,6 +159,8 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   using S = Shape<L, P, kMx>;
   constexpr int kShare = kWavesA / kGroups;      // waves that share out a head group's dimensions
   constexpr int kBlocks = L / 16 / kShare;       // blocks of 16 dimensions of a wave
+  // 8-bit rows and 128 heads: converted when the first product has left its registers (256 requests x 2048 rows 331 -> 215 us)
+  constexpr bool kLate = kMx && kGroups == 8 && L == 512;
   constexpr int kQueryTiles = (kGroups + 1) / 2; // the queries, as tiles of 32 heads
   extern __shared__ __align__(1024) char smem[];
   char* raw = smem + (kMx ? 2 * S::kTileBytes : 0);  // tiles as loaded (bf16: the tiles themselves)
@@ -298,7 +300,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
           if (from + i < S::kSteps)
-            k[from / kSet & 1][i][b] = *(const bf8*)(tile + kat[i & 1] + S::kColBytes * ((from + i) / 2) + 2048 * b);
+            k[from / kSet & 1][i][b] = *(const bf8*)(tile + kat[(from + i) & 1] + S::kColBytes * ((from + i) / 2) + 2048 * b);
     };
     read_keys(0);
     there[S::kAhead] = load(t + S::kAhead, next);  // into the place that every wave has left
@@ -309,7 +311,8 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       __syncthreads();
     }
     next = rows_of(t + S::kAhead + 1);
-    convert.read(raw + ((t + 1) & (kDepth - 1)) * S::kLoadBytes, tid);
+    const char* converted = raw + ((t + 1) & (kDepth - 1)) * S::kLoadBytes;
+    if constexpr (!kLate) convert.read(converted, tid);
     // S^T of 32 keys, 16 to a block
 #pragma unroll
     for (int j = 0; j < S::kSteps; ++j) {
@@ -327,10 +330,18 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       const char* at = tile + S::kColBytes * (d >> 2) + (kBlocks % 4 == 0 ? vat[b & 3] : vat[d & 3]);
       v[b % kReads] = read_across(at, at + 2048);
     };
+    if constexpr (kLate) {
+      int at = tid;
+      asm volatile("" : "+v"(at));  // places are worked out here: there are no registers to keep them in
+      __builtin_amdgcn_sched_barrier(0);
+      convert.read(converted, at);
+      convert.write(smem + ((t + 1) & 1) * S::kTileBytes, at);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int b = 0; b < kReads - 1; ++b)
       if (b < kBlocks) read_values(b);
-    convert.write(smem + ((t + 1) & 1) * S::kTileBytes, tid);
+    if constexpr (!kLate) convert.write(smem + ((t + 1) & 1) * S::kTileBytes, tid);
     if (there[0] != 0xffffffffu) {
       const uint32_t mask = there[0] >> (4 * group);
 #pragma unroll
