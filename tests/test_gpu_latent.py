@@ -552,6 +552,16 @@ def test_prompt_long(heads):
     sw.close()
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("rope", [32, 64])
+@pytest.mark.parametrize("nq,nk,heads", [([200], [200], 512), ([257, 3], [300, 9], 300), ([130], [4130], 64),
+                                         ([450, 540], [8400, 7000], 4)])
+def test_prompt_many_queries(nq, nk, heads, rope, causal):
+    """Enough of them for 256 queries to a workgroup, with 128 values; the keys of the last two in parts."""
+    sw, _ = _prompt_case(nq, nk, heads, 128, rope, 128, causal, seed=heads)
+    sw.close()
+
+
 @pytest.mark.parametrize("nope,rope,value", DIMS)
 @pytest.mark.parametrize("nq,nk,heads,causal", [([1], [5000], 1, True), ([40, 3, 0], [2600, 1400, 900], 2, True),
                                                 ([7, 90], [4000, 10], 1, False), ([130], [3333], 4, True)])
@@ -583,10 +593,10 @@ def test_prompt_keys_in_parts(nq, nk, heads, causal, nope, rope, value):
 
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
 @pytest.mark.parametrize("nope,rope,value", DIMS)
-@pytest.mark.parametrize("nq,nk", [([70, 300], [70, 300]), ([5, 40], [300, 77]), ([30], [2600])])
-def test_prompt_values_that_are_no_numbers(nq, nk, nope, rope, value, causal):
+@pytest.mark.parametrize("nq,nk,heads", [([70, 300], [70, 300], 2), ([5, 40], [300, 77], 2), ([30], [2600], 2),
+                                         ([200], [200], 512), ([130], [4130], 64)])
+def test_prompt_values_that_are_no_numbers(nq, nk, heads, nope, rope, value, causal):
     """An infinite value or a NaN reaches the queries that see its key, in its place, and nothing else."""
-    heads = 2
     sw, args = _prompt_case(nq, nk, heads, nope, rope, value, causal, seed=value, check=False)
     q, kv, rows, _, _, scale, o, lse, _ = args
     keys = []  # (sequence, key of it, head, place, what is there)
@@ -602,7 +612,7 @@ def test_prompt_values_that_are_no_numbers(nq, nk, nope, rope, value, causal):
     hm.hs_attend_prompt(sw.ctx, *args)
     for r in range(len(nq)):
         a, b, c, d = int(_cu(nq)[r]), int(_cu(nq)[r + 1]), int(starts[r]), int(starts[r + 1])
-        for h in range(heads):
+        for h in range(min(heads, 3)):
             w = ref.prompt(q[a:b, h].cpu().double(), clean[c:d, h], rows[c:d].cpu().double(), nope, scale, causal)
             got = o[a:b, h].clone()
             for rr, key, hh, place, _ in keys:
@@ -761,3 +771,73 @@ def test_prompt_and_decode_steps_together(mx):
             _within(od[r], want[0], want[2], f"step {step} request {r}")
             _within(lse[r], want[1], want[3], f"step {step} request {r}")
     sw.close()
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "8bit"])
+def test_captured_steps(mx):
+    """A decode step (map, store, selection, attention) captured once and replayed as its inputs move on, between eager
+    steps of another context with the same inputs, on a stream of their own: equal bits in everything written."""
+    R, k, B, T, H, heads, latent, rope = 5, 40, 64, 48, 200, 20, 512, 64
+    fmt = hm.row_format(latent, rope, int(mx))
+    gen = torch.Generator().manual_seed(31)
+    w = (1 + 0.1 * torch.randn(latent, generator=gen)).bfloat16().cuda()
+    f = (10000.0 ** (-2.0 * torch.arange(rope // 2, dtype=torch.float64) / rope)).cuda()
+    n = 2 * R  # room for two tokens of each request; some steps have fewer
+
+    class Steps:
+        def __init__(self):
+            self.sw = sw = hm.SwapIn(hm.config(R, k, B, 0.0, hm.hs_row_bytes(fmt), H, T))
+            self.new, self.length, self.tail0 = _ints([0] * R), _ints([0] * R), _ints([0] * R)
+            self.map, self.status = sw.map_buffers(n), torch.zeros(R, dtype=torch.int32, device="cuda")
+            self.x = torch.zeros(n, latent + rope, dtype=torch.bfloat16, device="cuda")
+            self.lat = torch.zeros_like(self.x)
+            self.topk = torch.full((R, k), -1, dtype=torch.int32, device="cuda")
+            self.out, self.miss, self.resolved = sw.outputs()[:3]
+            self.q = torch.zeros(R, heads, latent + rope, dtype=torch.bfloat16, device="cuda")
+            self.o = torch.zeros(R, heads, latent, dtype=torch.bfloat16, device="cuda")
+            self.lse = torch.zeros(R, heads, device="cuda")
+            self.work = sw.attend_work(fmt, heads)
+
+        def run(self, stream=None):
+            hm.hs_map_tokens(self.sw.ctx, self.new, self.length, self.tail0, *self.map, self.status, stream=stream)
+            hm.hs_store_rows(self.sw.ctx, fmt, self.x, w, 1e-6, f, *self.map[1:], self.lat, status=self.status,
+                             stream=stream)
+            hm.hs_resolve(self.sw.ctx, self.topk, self.tail0, self.out, self.miss, self.resolved, stream=stream)
+            hm.hs_attend(self.sw.ctx, fmt, self.q, 0.05, self.out, self.o, self.lse, work=self.work, stream=stream)
+
+        def written(self):
+            return [*self.map, self.status, self.lat, self.out, self.resolved, self.o, self.lse, self.sw.tail]
+
+    eager, captured = Steps(), Steps()
+    side = torch.cuda.Stream()
+    for c in (eager, captured):
+        c.sw.tail.zero_()
+    captured.run()  # (nothing: no token, no selection)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured.run()
+    length = [0] * R
+    for step in range(8):
+        new = [(step + r) % 3 for r in range(R)]
+        x, q = torch.randn(n, latent + rope, generator=gen), torch.randn(R, heads, latent + rope, generator=gen)
+        topk = torch.full((R, k), -1, dtype=torch.int32)
+        for r in range(R):
+            pick = torch.randperm(length[r] + new[r], generator=gen)[:k].to(torch.int32)
+            topk[r, :len(pick)] = pick
+        for c in (eager, captured):
+            c.new.copy_(_ints(new)), c.length.copy_(_ints(length)), c.topk.copy_(topk)
+            c.x.copy_(x), c.q.copy_(q)
+            c.lat.fill_(9)
+        torch.cuda.synchronize()
+        eager.run(side)
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(eager.written(), captured.written())):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), (step, i)
+        total = sum(new)
+        assert eager.map[0].tolist()[-1] == total and eager.status.tolist() == [0] * R
+        assert (eager.lat[total:] == 9).all()  # rows of no token
+        length = [a + b for a, b in zip(length, new)]
+    assert eager.o.abs().sum() > 0
+    eager.sw.close(), captured.sw.close()
