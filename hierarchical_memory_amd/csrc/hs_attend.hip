@@ -15,6 +15,7 @@
 #include "hs_mfma.h"
 
 #include <climits>
+#include <type_traits>
 #include <utility>
 
 namespace hs {
@@ -157,8 +158,10 @@ struct Converter<0, 0> {
 template <int L, int P, bool kMx, int kGroups>
 __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   using S = Shape<L, P, kMx>;
-  constexpr int kShare = kWavesA / kGroups;      // waves that share out a head group's dimensions
-  constexpr int kBlocks = L / 16 / kShare;       // blocks of 16 dimensions of a wave
+  constexpr int kShare = kWavesA / kGroups;      // waves of a head group
+  constexpr int kHalves = kGroups <= 2 ? 2 : 1;  // parts of a tile's keys; the waves of one share out the dimensions
+  constexpr int kKeyBlocks = 2 / kHalves;        // blocks of 16 keys of a wave
+  constexpr int kBlocks = L / 16 / (kShare / kHalves);  // blocks of 16 dimensions of a wave
   // 8-bit rows and 128 heads: converted when the first product has left its registers (256 requests x 2048 rows 331 -> 215 us)
   constexpr bool kLate = kMx && kGroups == 8 && L == 512;
   constexpr int kQueryTiles = (kGroups + 1) / 2; // the queries, as tiles of 32 heads
@@ -171,7 +174,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   const int col = lane & 15, group = lane >> 4;
   const Part part = part_of(a);
   const int head = part.h0 + (wave / kShare) * 16 + col;
-  const int share = wave % kShare;
+  const int share = wave % kShare / kHalves, key_half = wave % kHalves;
   const int rb = a.row.bytes;
   const int32_t* out = a.out + (size_t)part.r * a.k;
   // row i of the part's list: near + i * rb, or far + i * rb from index `edge` on
@@ -291,16 +294,17 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   for (int t = 0; t < tiles; ++t) {
     wait_tiles(std::integral_constant<int, kDepth - 2>());  // (8-bit rows: for tile t + 1)
     const char* tile = smem + (kMx ? t & 1 : t & (kDepth - 1)) * S::kTileBytes;
-    f4 s[2] = {};
+    const char* keys = tile + 2048 * key_half;
+    f4 s[kKeyBlocks] = {};
     constexpr int kSet = kGroups == 8 ? 2 : 4;  // k-steps whose rows are read before the steps before them are multiplied
-    bf8 k[2][kSet][2];
+    bf8 k[2][kSet][kKeyBlocks];
     auto read_keys = [&](int from) {
 #pragma unroll
       for (int i = 0; i < kSet; ++i)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kKeyBlocks; ++b)
           if (from + i < S::kSteps)
-            k[from / kSet & 1][i][b] = *(const bf8*)(tile + kat[(from + i) & 1] + S::kColBytes * ((from + i) / 2) + 2048 * b);
+            k[from / kSet & 1][i][b] = *(const bf8*)(keys + kat[(from + i) & 1] + S::kColBytes * ((from + i) / 2) + 2048 * b);
     };
     read_keys(0);
     there[S::kAhead] = load(t + S::kAhead, next);  // into the place that every wave has left
@@ -318,17 +322,18 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     for (int j = 0; j < S::kSteps; ++j) {
       if (j % kSet == 0) read_keys(j + kSet);
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < kKeyBlocks; ++b)
         s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[j / kSet & 1][j % kSet][b], q[j], s[b], 0, 0, 0);
       if (j % kSet == kSet - 1) __builtin_amdgcn_sched_barrier(0);
     }
     // the values' first blocks are on their way during the softmax, the others some blocks ahead of their product
     constexpr int kReads = kGroups == 8 ? 4 : 6;
-    bf8 v[kReads];
+    std::conditional_t<kHalves == 2, s4, bf8> v[kReads];
     auto read_values = [&](int b) {
       const int d = kBlocks * share + b;  // block of the row; vat is for its place in a group of columns
-      const char* at = tile + S::kColBytes * (d >> 2) + (kBlocks % 4 == 0 ? vat[b & 3] : vat[d & 3]);
-      v[b % kReads] = read_across(at, at + 2048);
+      const char* at = keys + S::kColBytes * (d >> 2) + (kBlocks % 4 == 0 ? vat[b & 3] : vat[d & 3]);
+      if constexpr (kHalves == 2) v[b % kReads] = read_across(at);
+      else v[b % kReads] = read_across(at, at + 2048);
     };
     if constexpr (kLate) {
       int at = tid;
@@ -343,15 +348,15 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       if (b < kBlocks) read_values(b);
     if constexpr (!kLate) convert.write(smem + ((t + 1) & 1) * S::kTileBytes, tid);
     if (there[0] != 0xffffffffu) {
-      const uint32_t mask = there[0] >> (4 * group);
+      const uint32_t mask = there[0] >> (4 * group + 16 * key_half);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i / 4][i % 4] = (mask >> (16 * (i / 4) + i % 4)) & 1 ? s[i / 4][i % 4] : -INFINITY;
+      for (int i = 0; i < 4 * kKeyBlocks; ++i) s[i / 4][i % 4] = (mask >> (16 * (i / 4) + i % 4)) & 1 ? s[i / 4][i % 4] : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < S::kAhead; ++i) there[i] = there[i + 1];
     float top = s[0][0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i / 4][i % 4]);
+    for (int i = 1; i < 4 * kKeyBlocks; ++i) top = fmaxf(top, s[i / 4][i % 4]);
     top = max_of_quarters(top) * scale;
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top);
@@ -367,45 +372,81 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     const float m0 = m == -INFINITY ? 0.0f : m;
     bf8 p;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) weigh_pair(s[i / 4][i % 4], s[i / 4][i % 4 + 1], scale, m0, p, i, sum, rsum);
+    for (int i = 0; i < 4 * kKeyBlocks; i += 2) weigh_pair(s[i / 4][i % 4], s[i / 4][i % 4 + 1], scale, m0, p, i, sum, rsum);
     __builtin_amdgcn_sched_barrier(0);
     // O^T
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
       if (b + kReads - 1 < kBlocks) read_values(b + kReads - 1);
-      o[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[b % kReads], p, o[b], 0, 0, 0);
+      if constexpr (kHalves == 2)
+        o[b] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v[b % kReads], __builtin_bit_cast(s8, p).lo, o[b], 0, 0, 0);
+      else
+        o[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[b % kReads], p, o[b], 0, 0, 0);
       if (b % 2 == 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads behind the last tile write to LDS too
+  wait_loads_and_meet<0>();  // the loads behind the last tile write to LDS too
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
   rsum += __shfl_xor(rsum, 16);
   rsum += __shfl_xor(rsum, 32);
+  constexpr int kOut = kBlocks / kHalves;  // blocks that the wave writes
+  f4 out_o[kOut];
+  if constexpr (kHalves == 2) {
+    // two waves have the same dimensions of both halves of the keys: each joins one half of the blocks, through LDS
+    constexpr int kStep = kAttendThreads;
+    static_assert((3 + 4 * kOut) * kStep * 4 <= (int)S::kLds);
+    float* const given = (float*)smem + wave * 64 + lane;
+    const float* const theirs = (const float*)smem + (wave ^ 1) * 64 + lane;
+    given[0] = m;
+    given[kStep] = sum;
+    given[2 * kStep] = rsum;
+#pragma unroll
+    for (int b = 0; b < kOut; ++b)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        out_o[b][j] = key_half ? o[kOut + b][j] : o[b][j];
+        given[(3 + 4 * b + j) * kStep] = key_half ? o[b][j] : o[kOut + b][j];
+      }
+    __syncthreads();
+    const float other = theirs[0], to = fmaxf(m, other);
+    const float c0 = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - to);
+    const float c1 = other == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(other - to);
+    m = to;
+    sum = sum * c0 + theirs[kStep] * c1;
+    rsum = rsum * c0 + theirs[2 * kStep] * c1;
+#pragma unroll
+    for (int b = 0; b < kOut; ++b)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out_o[b][j] = out_o[b][j] * c0 + theirs[(3 + 4 * b + j) * kStep] * c1;
+  } else {
+#pragma unroll
+    for (int b = 0; b < kOut; ++b) out_o[b] = o[b];
+  }
   if (head >= a.heads) return;
   const size_t rh = (size_t)part.r * a.heads + head;
-  const int first = 16 * kBlocks * share + 4 * group;  // of the lane's dimensions: 4 of every 16
+  const int first = 16 * kOut * (share * kHalves + key_half) + 4 * group;  // of the lane's dimensions: 4 of every 16
   if (a.splits == 1) {
     const float f = rsum > 0.0f ? 1.0f / rsum : rsum == 0.0f ? 0.0f : rsum;
     __bf16* dst = (__bf16*)a.o + rh * L + first;
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
+    for (int b = 0; b < kOut; ++b) {
       bf4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = (__bf16)(o[b][j] * f);
+      for (int j = 0; j < 4; ++j) v[j] = (__bf16)(out_o[b][j] * f);
       *(bf4*)(dst + 16 * b) = v;
     }
-    if (a.lse && share == 0 && group == 0)
+    if (a.lse && wave % kShare == 0 && group == 0)
       a.lse[rh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
     return;
   }
   // partial results: [R][heads][splits] of (m, sum, rsum, -) and [R][heads][splits][L]
   const size_t ph = rh * a.splits + part.split;
   const size_t stats = (size_t)a.R * a.heads * a.splits * 4;
-  if (share == 0 && group == 0) *(f4*)(a.work + ph * 4) = f4{m, sum, rsum, 0.0f};
+  if (wave % kShare == 0 && group == 0) *(f4*)(a.work + ph * 4) = f4{m, sum, rsum, 0.0f};
   float* dst = a.work + stats + ph * L + first;
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b) *(f4*)(dst + 16 * b) = o[b];
+  for (int b = 0; b < kOut; ++b) *(f4*)(dst + 16 * b) = out_o[b];
 }
 
 // Joins the parts of one request and head: a workgroup of four waves takes both, each wave every fourth part (all of a wave's

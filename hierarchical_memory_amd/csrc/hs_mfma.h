@@ -9,6 +9,7 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
 typedef float f16 __attribute__((ext_vector_type(16)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 #define HS_LDS __attribute__((address_space(3)))
@@ -81,10 +82,11 @@ __device__ __forceinline__ float max_of_quarters(float x) {
 
 // The matrix unit's first operand read across a tile's rows: lane (column d = lane % 32 of the 32 that `lo` begins) gets rows
 // 4 half + 0..3 (from lo) and 8 + 4 half + 0..3 (from hi) of the 16 that begin there, half = lane / 32.
+__device__ __forceinline__ s4 read_across(const char* at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(const HS_LDS char*)at);
+}
 __device__ __forceinline__ bf8 read_across(const char* lo, const char* hi) {
-  const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(const HS_LDS char*)lo);
-  const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((HS_LDS s4*)(const HS_LDS char*)hi);
-  return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(read_across(lo), read_across(hi), 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 // Where read_across reads in a group of columns for this lane: its row and chunk, for the first and second 32 columns and
