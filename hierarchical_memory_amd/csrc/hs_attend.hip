@@ -9,8 +9,13 @@
 //   S^T[key][head]  = K Q^T     A: the tile's rows from LDS, B: the queries, kept in registers
 //   O^T[dim][head] += V^T P^T   A: the same rows read through the transposing LDS load, B: the weights as S^T left them
 // (lane group g = lane / 16 holds the keys 4 g + 0..3 and 16 + 4 g + 0..3 of S^T; the second product takes its keys in that
-// order, so the weights never change lanes). With fewer than eight groups of 16 heads the waves of a group share out the
-// latent dimensions of the second product and each repeat the first.
+// order, so the weights never change lanes). With fewer than eight groups of 16 heads a group has more than one wave: half
+// of them take the first 16 keys of each tile, half the others (joined through LDS at the end), and the waves of a half share
+// out the latent dimensions of the second product and repeat the first. LDS reads bound it there: with all 32 keys to each
+// wave 256 requests x 2048 rows take 130 us for 16 heads and 146 for 64, with halves 112 and 127 (5.5 and 5.0 TB/s of rows,
+// what memory gives); 64 heads of 8-bit rows 152 and 139. With 128 heads 172 us (3.9 TB/s, 850 TFLOP/s): a tile's loads alone
+// take 130, and the two products' dependence and the waves' meeting at each tile keep them from hiding all of the rest.
+// 8-bit rows are converted to bf16 tiles, so their products cost the same, and what they spare in bytes shows only in part.
 #include "hs_latent.h"
 #include "hs_mfma.h"
 
@@ -159,11 +164,12 @@ template <int L, int P, bool kMx, int kGroups>
 __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   using S = Shape<L, P, kMx>;
   constexpr int kShare = kWavesA / kGroups;      // waves of a head group
-  constexpr int kHalves = kGroups <= 2 ? 2 : 1;  // parts of a tile's keys; the waves of one share out the dimensions
+  constexpr int kHalves = kGroups <= 4 ? 2 : 1;  // parts of a tile's keys; the waves of one share out the dimensions
   constexpr int kKeyBlocks = 2 / kHalves;        // blocks of 16 keys of a wave
   constexpr int kBlocks = L / 16 / (kShare / kHalves);  // blocks of 16 dimensions of a wave
-  // 8-bit rows and 128 heads: converted when the first product has left its registers (256 requests x 2048 rows 331 -> 215 us)
-  constexpr bool kLate = kMx && kGroups == 8 && L == 512;
+  // 8-bit rows and many heads: converted when the first product has left its registers (256 requests x 2048 rows x 128 heads
+  // 331 -> 215 us)
+  constexpr bool kLate = kMx && kGroups >= 4 && L == 512;
   constexpr int kQueryTiles = (kGroups + 1) / 2; // the queries, as tiles of 32 heads
   extern __shared__ __align__(1024) char smem[];
   char* raw = smem + (kMx ? 2 * S::kTileBytes : 0);  // tiles as loaded (bf16: the tiles themselves)
