@@ -369,8 +369,8 @@ int hs_map_tokens(hs_ctx* ctx, const int32_t* d_new, const int32_t* d_len, const
  * x = d_pos[t] >= 0 and row input d_x[t * x_stride .. + latent + rope) (bf16):
  *   y = latent part / sqrt(mean of its squares + eps) * d_weight (bf16 [latent]), in 32 bits
  *   z = rope part with its pairs (HS_ROPE_PAIRS: (2i, 2i + 1), HS_ROPE_HALVES: (i, i + rope / 2)) turned by the angle
- *       x * d_freqs[i] (radians, [rope / 2] double, 8-byte aligned; the angle is reduced in 64 bits, so positions of
- *       any size turn exactly); d_freqs NULL: as they are
+ *       x * d_freqs[i] (radians, [rope / 2] double, 8-byte aligned; the angle is reduced in 64 bits, so far positions
+ *       turn as precisely as near ones); d_freqs NULL: as they are
  *   the row of the context's format from y and z, each value rounded once. HS_ROW_MXFP8: a block's scale is the least
  *       power of two (at least 2^-100) that keeps it within 448.
  * d_slot[t] in [B, B + T): the row becomes row d_slot[t] - B of the request's device tail. d_slot[t] == -1: it becomes
@@ -405,9 +405,10 @@ int hs_store_rows(hs_ctx* ctx, const hs_row_format* fmt, const void* d_x, int64_
  *   d_work    hs_attend_work_bytes bytes of device memory, 16-byte aligned (NULL where that is 0), free again when the
  *             call's work on the stream has completed. Calls that may overlap (two streams, two captured graphs) need
  *             one each. Nothing in it has to start at zero.
- * Scores, sums and partial results are held in 32 bits; the softmax weights are rounded to bf16 for the product
- * with the rows (the sum that divides it is that of the rounded weights), the result once to bf16. The order of every sum is fixed, so equal inputs give equal bits. scale must
- * be finite. Rows that are not selected are not read, so nothing in them reaches the result.
+ * Scores, sums and partial results are held in 32 bits; the softmax weights are rounded to bf16 for the product with the
+ * rows (the sum that divides it is that of the rounded weights), the result once to bf16. The order of every sum is fixed,
+ * so equal inputs give equal bits. scale must be finite. Rows that are not selected are not read, so nothing in them
+ * reaches the result.
  */
 int hs_attend_work_bytes(const hs_config* cfg, const hs_row_format* fmt, int32_t heads, uint64_t* bytes);
 int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t heads, float scale, const int32_t* d_out,
