@@ -320,6 +320,15 @@ def test_attend(R, k, B, T, heads, pad, empty, gathered, latent, rope, mx):
 
 
 @pytest.mark.parametrize("mx", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("k,heads,latent,rope", [(2100, 16, 256, 32), (1100, 64, 512, 64), (1100, 128, 512, 64)])
+def test_attend_whole_selections(k, heads, latent, rope, mx):
+    """Enough requests that each selection stays in one part, longer than what is listed at a time."""
+    c = Attend(256, k, k, 0, heads, latent, rope, mx, seed=heads, pad=0.02)
+    assert c.work is None
+    c.run().check({0, 100, 255}).close()
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "8bit"])
 def test_attend_only_selected_rows_are_read(mx):
     """NaN and infinities in every row that is not selected, and indices outside the row space."""
     c = Attend(3, 70, 90, 20, 20, 512, 64, mx, seed=5, pad=0.1)
@@ -622,6 +631,29 @@ def test_prompt_values_that_are_no_numbers(nq, nk, heads, nope, rope, value, cau
                     got[first:, place], w[0][first:, place] = 0.0, 0.0
             _within(got, w[0], w[2], f"sequence {r} head {h} o")
             _within(lse[a:b, h], w[1], w[3], f"sequence {r} head {h} lse")
+
+
+@pytest.mark.parametrize("nq,nk", [([1, 40], [66000, 70]), ([90000, 40], [1, 70])], ids=["keys", "queries"])
+def test_prompt_offsets_past_4_gib(nq, nk):
+    heads, nope, rope, value = 128, 128, 64, 128
+    sw = hm.SwapIn(hm.config(2, 1, 1, 0.0, 16, 4, 0))
+    gen = torch.Generator().manual_seed(40)
+    q = torch.zeros(sum(nq), heads, nope + rope, dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros(sum(nk), heads, nope + value, dtype=torch.bfloat16, device="cuda")
+    kr = torch.zeros(sum(nk), rope, dtype=torch.bfloat16, device="cuda")
+    o = torch.full((sum(nq), heads, value), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((sum(nq), heads), 9.0, device="cuda")
+    assert max(q.numel(), kv.numel()) * 2 > 1 << 32
+    last_q, last_kv, last_kr = (torch.randn(n, *x.shape[1:], generator=gen).bfloat16()
+                                for n, x in ((nq[1], q), (nk[1], kv), (nk[1], kr)))
+    q[nq[0]:], kv[nk[0]:], kr[nk[0]:] = last_q.cuda(), last_kv.cuda(), last_kr.cuda()
+    hm.hs_attend_prompt(sw.ctx, q, kv, kr, _cu(nq).cuda(), _cu(nk).cuda(), 0.07, o, lse)
+    for h in (0, 63, 127):
+        w = ref.prompt(last_q[:, h].double(), last_kv[:, h].double(), last_kr.double(), nope, 0.07, True)
+        _within(o[nq[0]:, h], w[0], w[2], f"head {h} o")
+        _within(lse[nq[0]:, h], w[1], w[3], f"head {h} lse")
+    assert not o[:nq[0]].any()  # no key, or keys of zeros
+    sw.close()
 
 
 def test_prompt_many_sequences():
