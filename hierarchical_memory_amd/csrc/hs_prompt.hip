@@ -142,12 +142,15 @@ __device__ __forceinline__ bool find_item(const PromptArgs& a, int id, Item* it,
     const Sequence q = sequence(r0 - tid);
     const int parts = a.splits > 1 ? parts_of(q.nk, per) : 1;
     const int c = q.tiles * parts;
+    // inclusive sums over the wave by lane shifts: 1, 2, 4, 8 in each row of 16, then lane 15 into the rows 1 and 3, lane 31
+    // into the rows 2 and 3
     int x = c;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(x, d);
-      if (lane >= d) x += y;
-    }
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
     if (lane == 63) sh[wave] = x;
     if (tid == 0) sh[kWaves] = 0;
     __syncthreads();
@@ -213,35 +216,9 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
     const int t0 = (int)((int64_t)all * it.part / it.parts), t1 = (int)((int64_t)all * (it.part + 1) / it.parts);
 
     const int wq = first + wave * 32 * kSets;  // the wave's first query
-    int limit[kSets];                           // keys that the lane's queries see
-    bf8 q[kSets][S::kSteps];
-#pragma unroll
-    for (int g = 0; g < kSets; ++g) {
-      const int i = wq + 32 * g + col, j = i < nq ? i : nq - 1;
-      limit[g] = a.causal ? cut(nk - nq + j + 1, nk) : nk;
-      const __bf16* src = (const __bf16*)a.q + ((size_t)(q0 + j) * a.heads + h) * (DN + P) + 8 * half;
-#pragma unroll
-      for (int s = 0; s < S::kSteps; ++s) {
-        q[g][s] = turned(*(const v4u*)(src + 16 * s), sign);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < kSets; ++g)
-#pragma unroll
-      for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+a"(q[g][s]));
     // of the wave: keys that all of its queries see, and that any does
     const int lo = a.causal ? cut(nk - nq + wq + 1, nk) : nk;
     const int hi = a.causal ? cut(nk - nq + wq + 32 * kSets, nk) : nk;
-
-    f16 o[kSets][kBlocks];
-    float m[kSets], sum[kSets], rsum[kSets];
-#pragma unroll
-    for (int g = 0; g < kSets; ++g) {
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) o[g][b] = f16{};
-      m[g] = -INFINITY;
-      sum[g] = rsum[g] = 0.0f;
-    }
 
     // the lane's chunk of one key of every tile
     const int mine = 8 * wave + (lane >> 3), place = (lane & 7) ^ swizzle(mine);
@@ -262,6 +239,41 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       }
       place_in = place_in + 1 < S::kDepth ? place_in + 1 : 0;
     };
+    // (128 queries: on their way with the queries, 64 prompts of up to 300 tokens 57 -> 55 us; with 256 the registers that
+    // wait for both cost more than they hide, 8192 tokens x 16 heads 360 -> 370)
+    auto load_first = [&]() {
+#pragma unroll
+      for (int i = 0; i < S::kDepth - 2; ++i)
+        if (t0 + i < t1) load(t0 + i);
+    };
+    if constexpr (kSets == 1) load_first();
+
+    int limit[kSets];                           // keys that the lane's queries see
+    bf8 q[kSets][S::kSteps];
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+      const int i = wq + 32 * g + col, j = i < nq ? i : nq - 1;
+      limit[g] = a.causal ? cut(nk - nq + j + 1, nk) : nk;
+      const __bf16* src = (const __bf16*)a.q + ((size_t)(q0 + j) * a.heads + h) * (DN + P) + 8 * half;
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) {
+        q[g][s] = turned(*(const v4u*)(src + 16 * s), sign);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kSets; ++g)
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) asm volatile("" : "+a"(q[g][s]));
+    f16 o[kSets][kBlocks];
+    float m[kSets], sum[kSets], rsum[kSets];
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) o[g][b] = f16{};
+      m[g] = -INFINITY;
+      sum[g] = rsum[g] = 0.0f;
+    }
+
     // An infinite value or a NaN of a key that some of the workgroup's queries see and others do not would reach those too (a
     // weight of zero makes it NaN): the lane takes such ones out of its chunks of the tile, and the queries that see them
     // get them at the end. Only tiles that some query does not see whole are looked through (8192 tokens x 16 heads: no
@@ -429,9 +441,7 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
     };
 
     if (t0 < t1) {
-#pragma unroll
-      for (int i = 0; i < S::kDepth - 2; ++i)
-        if (t0 + i < t1) load(t0 + i);
+      if constexpr (kSets == 2) load_first();
       next_tile(t0);
       const int begin = S::kPer * t0;
       if (begin < mine_end) {
