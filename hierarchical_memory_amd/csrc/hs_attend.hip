@@ -118,43 +118,57 @@ struct Converter {
   v4u values[L / 256], rope;
   uint32_t scales[L / 256];
 
-  __device__ __forceinline__ void read(const char* raw, int tid) {
+  static constexpr int kParts = L / 256 + 1;  // of the values, and the rope part's
+
+  __device__ __forceinline__ void read(int part, const char* raw, int tid) {
     const int row = tid >> 4, c = tid & 15;
     auto chunk = [&](int q) {  // of the row, which may lie in its rest
       return q < 8 * S::kRawCols ? raw + (q >> 3) * S::kColBytes + row * 128 + (q & 7) * 16
                                  : raw + S::kRawCols * S::kColBytes + (row * S::kRawRest + q - 8 * S::kRawCols) * 16;
     };
-#pragma unroll
-    for (int j = 0; j < L / 256; ++j) {
-      values[j] = *(const v4u*)chunk(16 * j + c);
-      scales[j] = ((const uint32_t*)chunk(S::kScales / 16))[2 * j + (c >> 3)];
+    if (part == kParts - 1) {
+      rope = *(const v4u*)chunk(S::kRope / 16 + (c & (P / 8 - 1)));
+      return;
     }
-    rope = *(const v4u*)chunk(S::kRope / 16 + (c & (P / 8 - 1)));
+    values[part] = *(const v4u*)chunk(16 * part + c);
+    scales[part] = ((const uint32_t*)chunk(S::kScales / 16))[2 * part + (c >> 3)];
   }
 
-  __device__ __forceinline__ void write(char* tile, int tid) const {
+  __device__ __forceinline__ void write(int part, char* tile, int tid) const {
     const int row = tid >> 4, c = tid & 15, f = swizzle16(row);
-#pragma unroll
-    for (int j = 0; j < L / 256; ++j) {
-      const float scale = __uint_as_float(((scales[j] >> (8 * ((c >> 1) & 3))) & 255u) << 23);
-      v4u y[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = values[j][i];
-        y[i / 2][i % 2 * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, false));
-        y[i / 2][i % 2 * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, true));
-      }
-      // neighbouring groups of columns in opposite order, to other banks
-      char* to = tile + (4 * j + (c >> 2)) * S::kColBytes + row * 128;
-      const int first = (c >> 2) & 1;
-      *(v4u*)(to + (((2 * (c & 3) + first) ^ f) << 4)) = first ? y[1] : y[0];
-      *(v4u*)(to + (((2 * (c & 3) + 1 - first) ^ f) << 4)) = first ? y[0] : y[1];
+    if (part == kParts - 1) {
+      if (c < P / 8) *(v4u*)(tile + L / 64 * S::kColBytes + row * 128 + ((c ^ f) << 4)) = rope;
+      return;
     }
-    if (c < P / 8) *(v4u*)(tile + L / 64 * S::kColBytes + row * 128 + ((c ^ f) << 4)) = rope;
+    const float scale = __uint_as_float(((scales[part] >> (8 * ((c >> 1) & 3))) & 255u) << 23);
+    v4u y[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = values[part][i];
+      y[i / 2][i % 2 * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, false));
+      y[i / 2][i % 2 * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, true));
+    }
+    // neighbouring groups of columns in opposite order, to other banks
+    char* to = tile + (4 * part + (c >> 2)) * S::kColBytes + row * 128;
+    const int first = (c >> 2) & 1;
+    *(v4u*)(to + (((2 * (c & 3) + first) ^ f) << 4)) = first ? y[1] : y[0];
+    *(v4u*)(to + (((2 * (c & 3) + 1 - first) ^ f) << 4)) = first ? y[0] : y[1];
+  }
+
+  __device__ __forceinline__ void read(const char* raw, int tid) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) read(i, raw, tid);
+  }
+  __device__ __forceinline__ void write(char* tile, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) write(i, tile, tid);
   }
 };
 template <>
 struct Converter<0, 0> {
+  static constexpr int kParts = 0;
+  __device__ __forceinline__ void read(int, const char*, int) {}
+  __device__ __forceinline__ void write(int, char*, int) const {}
   __device__ __forceinline__ void read(const char*, int) {}
   __device__ __forceinline__ void write(char*, int) const {}
 };
@@ -168,7 +182,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   constexpr int kKeyBlocks = 2 / kHalves;        // blocks of 16 keys of a wave
   constexpr int kBlocks = L / 16 / (kShare / kHalves);  // blocks of 16 dimensions of a wave
   // 8-bit rows and many heads: converted when the first product has left its registers (256 requests x 2048 rows x 128 heads
-  // 331 -> 215 us)
+  // 331 -> 207 us)
   constexpr bool kLate = kMx && kGroups >= 4 && L == 512;
   constexpr int kQueryTiles = (kGroups + 1) / 2; // the queries, as tiles of 32 heads
   extern __shared__ __align__(1024) char smem[];
@@ -343,11 +357,14 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     };
     if constexpr (kLate) {
       int at = tid;
-      asm volatile("" : "+v"(at));  // places are worked out here: there are no registers to keep them in
+      asm volatile("" : "+v"(at));  // places are worked out here, and parts one by one: registers are short
       __builtin_amdgcn_sched_barrier(0);
-      convert.read(converted, at);
-      convert.write(smem + ((t + 1) & 1) * S::kTileBytes, at);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < convert.kParts; ++i) {
+        convert.read(i, converted, at);
+        convert.write(i, smem + ((t + 1) & 1) * S::kTileBytes, at);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
 #pragma unroll
     for (int b = 0; b < kReads - 1; ++b)
