@@ -13,7 +13,7 @@
 // of them take the first 16 keys of each tile, half the others (joined through LDS at the end), and the waves of a half share
 // out the latent dimensions of the second product and repeat the first. LDS reads bound it there: with all 32 keys to each
 // wave 256 requests x 2048 rows take 130 us for 16 heads and 146 for 64, with halves 112 and 127 (5.5 and 5.0 TB/s of rows,
-// what memory gives); 64 heads of 8-bit rows 152 and 139. With 128 heads 172 us (3.9 TB/s, 850 TFLOP/s): a tile's loads alone
+// what memory gives); 64 heads of 8-bit rows 152 and 133. With 128 heads 172 us (3.9 TB/s, 850 TFLOP/s): a tile's loads alone
 // take 130, and the two products' dependence and the waves' meeting at each tile keep them from hiding all of the rest.
 // 8-bit rows are converted to bf16 tiles, so their products cost the same, and what they spare in bytes shows only in part.
 #include "hs_latent.h"
@@ -79,6 +79,16 @@ __device__ __forceinline__ void load_half(bool odd, const char* row, const char*
     load_groups<1, kCols, kHalf, kGroupBytes>(row, last, lds, std::make_integer_sequence<int, kCols / 2>());
   else
     load_groups<0, kCols, kHalf, kGroupBytes>(row, last, lds, std::make_integer_sequence<int, (kCols + 1) / 2>());
+}
+
+// All but the last `later` tiles asked for (at most kMost) are in LDS, for every wave.
+template <int kMost, class S>
+__device__ __forceinline__ void wait_tiles(bool odd, int later) {
+  if constexpr (kMost > 0) {
+    if (later < kMost) return wait_tiles<kMost - 1, S>(odd, later);
+  }
+  if (odd) wait_loads_and_meet<S::kOdd * kMost>();
+  else wait_loads_and_meet<S::kEven * kMost>();
 }
 
 struct Part { int r, split, h0, begin, end; };
@@ -182,7 +192,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   constexpr int kKeyBlocks = 2 / kHalves;        // blocks of 16 keys of a wave
   constexpr int kBlocks = L / 16 / (kShare / kHalves);  // blocks of 16 dimensions of a wave
   // 8-bit rows and many heads: converted when the first product has left its registers (256 requests x 2048 rows x 128 heads
-  // 331 -> 207 us)
+  // 331 -> 185 us)
   constexpr bool kLate = kMx && kGroups >= 4 && L == 512;
   constexpr int kQueryTiles = (kGroups + 1) / 2; // the queries, as tiles of 32 heads
   extern __shared__ __align__(1024) char smem[];
@@ -221,8 +231,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       list[i * kAttendThreads + tid] = there ? (a.gather ? at : s[i]) : -1;
     }
   };
-  // asks for tile t (behind the last one: whatever the list holds, so that every tile is the same number of loads) and says
-  // which of its rows are there
+  // asks for tile t and says which of its rows are there
   const bool odd = wave >= kWavesA / 2;
   const int mine = 8 * (wave & 3) + (lane >> 3), place = (lane & 7) ^ swizzle16(mine);
   const int rest_mine = (8 * (wave & 3) + lane / S::kRawRest) & (kTile - 1), rest_place = lane % S::kRawRest;
@@ -251,12 +260,6 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     }
     return (uint32_t)__ballot(r.lane >= 0);
   };
-  auto wait_tiles = [&](auto later) {  // all but the last `later` tiles asked for are in LDS, for every wave
-    constexpr int n = decltype(later)::value;
-    if (odd) wait_loads_and_meet<S::kOdd * n>();
-    else wait_loads_and_meet<S::kEven * n>();
-  };
-
   // LDS places of this lane's reads, but for the tile's start
   int kat[2], vat[4];
 #pragma unroll
@@ -271,7 +274,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   // the list of rows is on its way at the same time, and so are then the tiles whose places the queries leave.
   constexpr int kQueryAt = kMx ? 0 : kDepth - kQueryTiles;  // tile place
   constexpr int kEarly = kMx ? (kQueryTiles <= 2 ? S::kAhead : 0) : (kQueryAt < S::kAhead ? kQueryAt : S::kAhead);
-  uint32_t there[S::kAhead + 1];  // of the tiles asked for, the one in use first
+  uint32_t there[S::kAhead + 1] = {};  // of the tiles asked for, the one in use first
   bf8 q[S::kSteps];
   {
     int s[kPer];
@@ -286,7 +289,8 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     write_list(0, s);
     wait_loads_and_meet<0>();
 #pragma unroll
-    for (int t = 0; t < kEarly; ++t) there[t] = load(t, rows_of(t));
+    for (int t = 0; t < kEarly; ++t)
+      if (t < tiles) there[t] = load(t, rows_of(t));
     const char* tile = smem + (kQueryAt + wave / kShare / 2) * S::kTileBytes + wave / kShare % 2 * 2048;
     const uint32_t sign = a.scale < 0.0f ? kSigns : 0u;
 #pragma unroll
@@ -296,7 +300,8 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     for (int i = 0; i < S::kSteps; ++i) asm volatile("" : "+v"(q[i]));  // read, before others write there
     asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-    for (int t = kEarly; t < S::kAhead; ++t) there[t] = load(t, rows_of(t));
+    for (int t = kEarly; t < S::kAhead; ++t)
+      if (t < tiles) there[t] = load(t, rows_of(t));
   }
   f4 o[kBlocks];
 #pragma unroll
@@ -306,13 +311,13 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   Converter<kMx ? L : 0, kMx ? P : 0> convert;
   Rows next = rows_of(S::kAhead);
   if constexpr (kMx) {
-    wait_tiles(std::integral_constant<int, kDepth - 1>());
+    wait_tiles<kDepth - 1, S>(odd, tiles - 1);
     convert.read(raw, tid);
     convert.write(smem, tid);
   }
 
   for (int t = 0; t < tiles; ++t) {
-    wait_tiles(std::integral_constant<int, kDepth - 2>());  // (8-bit rows: for tile t + 1)
+    wait_tiles<kDepth - 2, S>(odd, tiles - 1 - t - (kMx ? 1 : 0));  // (8-bit rows: for tile t + 1)
     const char* tile = smem + (kMx ? t & 1 : t & (kDepth - 1)) * S::kTileBytes;
     const char* keys = tile + 2048 * key_half;
     f4 s[kKeyBlocks] = {};
@@ -327,8 +332,8 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
             k[from / kSet & 1][i][b] = *(const bf8*)(keys + kat[(from + i) & 1] + S::kColBytes * ((from + i) / 2) + 2048 * b);
     };
     read_keys(0);
-    there[S::kAhead] = load(t + S::kAhead, next);  // into the place that every wave has left
-    if ((t + S::kAhead + 1) * kTile % kListed == 0) {  // every wave has read all that the list named
+    if (t + S::kAhead < tiles) there[S::kAhead] = load(t + S::kAhead, next);  // into the place that every wave has left
+    if ((t + S::kAhead + 1) * kTile % kListed == 0 && t + S::kAhead + 1 < tiles) {  // every wave has read all that the list named
       int more[kPer];
       read_list((t + S::kAhead + 1) * kTile, more);
       write_list((t + S::kAhead + 1) * kTile, more);
@@ -355,7 +360,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       if constexpr (kHalves == 2) v[b % kReads] = read_across(at);
       else v[b % kReads] = read_across(at, at + 2048);
     };
-    if constexpr (kLate) {
+    if (kLate && t + 1 < tiles) {
       int at = tid;
       asm volatile("" : "+v"(at));  // places are worked out here, and parts one by one: registers are short
       __builtin_amdgcn_sched_barrier(0);
@@ -408,7 +413,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       if (b % 2 == 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
-  wait_loads_and_meet<0>();  // the loads behind the last tile write to LDS too
+  wait_loads_and_meet<0>();  // every wave has left the tiles, and what it wrote there
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
   rsum += __shfl_xor(rsum, 16);
