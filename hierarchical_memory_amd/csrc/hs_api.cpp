@@ -839,7 +839,9 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
   if (need > 0 && (!d_work || work_bytes < need))
     return fail(HS_E_INVALID, "work buffer has %llu bytes, needs %llu", (unsigned long long)(d_work ? work_bytes : 0),
                 (unsigned long long)need);
-  a.splits = hs::attend_splits(a.R, a.k, heads, a.row);
+  const hs::AttendPlan plan = hs::attend_plan(a.R, a.k, heads, a.row);
+  a.groups = plan.groups;
+  a.splits = plan.splits;
   a.scale = scale;
   a.q = (const uint16_t*)d_q;
   a.out = d_out;

@@ -32,7 +32,6 @@ constexpr int kWavesA = kAttendThreads / 64;
 constexpr int kTile = 32;          // rows of a tile
 constexpr int kDepth = 4;          // tiles in LDS as memory has them: one in use, the others on their way
 constexpr int kListed = 1024;      // rows of the selection whose indices are held in LDS at a time
-constexpr int kGroupHeads = 128;   // most heads of one workgroup
 constexpr int kMostSplits = 64;    // parts of a selection: one to a lane of the wave that joins them
 __device__ __align__(16) uint4 zero_row[72];  // what a tile holds where there is no row
 
@@ -93,6 +92,8 @@ __device__ __forceinline__ void wait_tiles(bool odd, int later) {
 
 struct Part { int r, split, h0, begin, end; };
 
+// kGroupHeads: heads of a workgroup
+template <int kGroupHeads>
 __device__ __forceinline__ Part part_of(const AttendArgs& a) {
   Part p;
   const int groups = (a.heads + kGroupHeads - 1) / kGroupHeads;
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
   const uint32_t raw0 = smem0 + (uint32_t)(raw - smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, group = lane >> 4;
-  const Part part = part_of(a);
+  const Part part = part_of<16 * kGroups>(a);
   const int head = part.h0 + (wave / kShare) * 16 + col;
   const int share = wave % kShare / kHalves, key_half = wave % kHalves;
   const int rb = a.row.bytes;
@@ -539,15 +540,15 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
 template <int L, int P, bool kMx, int kGroups>
 void launch(const AttendArgs& a, hipStream_t s) {
   constexpr uint32_t lds = Shape<L, P, kMx>::kLds;
-  const int groups = (a.heads + kGroupHeads - 1) / kGroupHeads;
+  const int groups = (a.heads + 16 * kGroups - 1) / (16 * kGroups);
   hipLaunchKernelGGL((attend_kernel<L, P, kMx, kGroups>), dim3(a.R * groups * a.splits), dim3(kAttendThreads), lds, s, a);
 }
 
 template <int L, int P, bool kMx>
 hipError_t launch_heads(const AttendArgs& a, hipStream_t s) {
-  if (a.heads <= 16) launch<L, P, kMx, 1>(a, s);
-  else if (a.heads <= 32) launch<L, P, kMx, 2>(a, s);
-  else if (a.heads <= 64) launch<L, P, kMx, 4>(a, s);
+  if (a.groups == 1) launch<L, P, kMx, 1>(a, s);
+  else if (a.groups == 2) launch<L, P, kMx, 2>(a, s);
+  else if (a.groups == 4) launch<L, P, kMx, 4>(a, s);
   else launch<L, P, kMx, 8>(a, s);
   if (a.splits > 1)
     hipLaunchKernelGGL(join_kernel<L>, dim3(a.R * a.heads), dim3(256), 0, s, a);
@@ -566,30 +567,36 @@ hipError_t set_lds() {
 
 }  // namespace
 
-// Parts of each selection: the number for which a model of the call's time, in tenths of a microsecond, is least. A
-// workgroup takes 6 us to begin and end and 1.8 us a tile when all 256 compute units stream rows; the join takes 4 us and
-// the time that the partial results take to memory and back (at 5 TB/s). Measured against it, in us: 64 requests x 2048
-// rows x 64 heads in 3, 4, 6, 8 parts 60 (modelled) / 55, 78, 73; 32 x 2048 x 16 in 6, 8, 12 parts 24, 23, 31; 7 x 999 x 20
-// in 8, 16, 32 parts 11, 10, 10.
-int attend_splits(int R, int k, int heads, const RowLayout& row) {
-  const int64_t units = (int64_t)R * ((heads + kGroupHeads - 1) / kGroupHeads);
+// Heads of a workgroup and parts of each selection: those for which a model of the call's time, in tenths of a microsecond, is
+// least. A workgroup takes 5.5 to 9 us to begin and end and 1.7 to 2.7 a tile, by its heads, when all 256 compute units
+// stream rows; the join takes 4 us, some more by the parts, and the time that the partial results take to memory and back
+// (at 5 TB/s). Measured, in us: 64 requests x 2048 rows x 64 heads (8 bits) in 3, 4, 6, 8 parts 59, 53 (modelled), 73, 69; 32 x
+// 2048 x 16 in 6, 8, 12 parts 23, 23 (modelled), 30. Few requests with many heads take fewer heads to a workgroup, which read
+// the same rows (from the caches): 128, 64, 32, 16 heads to one: 1 x 2048 x 128 heads 24.8, 20.9, 17.5, 16.0; 4 x 2048 x 128
+// 29, 26, 22, 24; 256 x 64 x 128 24, 33, 41, 59.
+AttendPlan attend_plan(int R, int k, int heads, const RowLayout& row) {
   const int tiles = (k + kTile - 1) / kTile;
-  int best = 1;
+  AttendPlan best{1, 1};
   int64_t least = INT64_MAX;
-  for (int s = 1; s <= tiles && s <= kMostSplits; ++s) {
-    const int64_t rounds = (units * s + 255) / 256, per = (tiles + s - 1) / s;
-    int64_t t = rounds * (per * 18 + 60);
-    if (s > 1) t += 40 + (int64_t)R * heads * s * row.latent * 8 / 500000;
-    if (t < least) {
-      least = t;
-      best = s;
+  for (int g = 8; g >= 1; g /= 2) {
+    if (g > 1 && heads <= 8 * g) continue;  // half as many would do
+    const int64_t units = (int64_t)R * ((heads + 16 * g - 1) / (16 * g));
+    const int tile = g == 8 ? 27 : g == 4 ? 20 : g == 2 ? 18 : 17, start = g == 8 ? 90 : g == 4 ? 70 : g == 2 ? 60 : 55;
+    for (int s = 1; s <= tiles && s <= kMostSplits; ++s) {
+      const int64_t rounds = (units * s + 255) / 256, per = (tiles + s - 1) / s;
+      int64_t t = rounds * (per * tile + start);
+      if (s > 1) t += 40 + 4 * s / 5 + (int64_t)R * heads * s * row.latent * 8 / 500000;
+      if (t < least) {
+        least = t;
+        best = AttendPlan{g, s};
+      }
     }
   }
   return best;
 }
 
 uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row) {
-  const uint64_t s = (uint64_t)attend_splits(R, k, heads, row);
+  const uint64_t s = (uint64_t)attend_plan(R, k, heads, row).splits;
   return s == 1 ? 0 : (uint64_t)R * heads * s * (16 + 4ull * row.latent);
 }
 

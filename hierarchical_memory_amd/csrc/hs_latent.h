@@ -65,6 +65,7 @@ struct StoreArgs {
 struct AttendArgs {
   RowLayout row;
   int32_t R, k, B, T, heads;
+  int32_t groups;         // groups of 16 heads to a workgroup (1, 2, 4 or 8)
   int32_t splits;         // parts of the selection, each a workgroup's
   float scale;
   const uint16_t* q;      // [R][heads][latent + rope] bf16
@@ -94,8 +95,12 @@ struct PromptArgs {
   float* work;            // partial results where splits > 1
 };
 
-// Parts that hs_attend cuts a selection of k rows into, and the bytes of their partial results.
-int attend_splits(int R, int k, int heads, const RowLayout& row);
+// How hs_attend shares out its work: groups of 16 heads to a workgroup and parts of each selection; and the bytes of the
+// parts' results.
+struct AttendPlan {
+  int groups, splits;
+};
+AttendPlan attend_plan(int R, int k, int heads, const RowLayout& row);
 uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row);
 
 // The same for hs_attend_prompt.

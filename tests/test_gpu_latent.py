@@ -308,6 +308,14 @@ ATTENDS = [  # (R, k, B, T, heads, pad, empty, gathered)
     (40, 300, 320, 10, 8, 0.9, (3, 39), False),
     (300, 17, 20, 3, 16, 0.3, (299,), False),
     (1, 2048, 2100, 0, 16, 0.0, (), False),
+    # enough requests that a workgroup takes 64, or 128, heads; the last two with selections in parts
+    (200, 65, 80, 16, 33, 0.5, (1,), False),
+    (200, 90, 100, 0, 64, 0.1, (0, 199), True),
+    (180, 57, 70, 5, 100, 0.2, (90,), False),
+    (200, 33, 40, 0, 128, 0.0, (), False),
+    (150, 65, 80, 9, 129, 0.3, (1,), False),
+    (64, 1500, 1510, 7, 60, 0.05, (63,), False),
+    (64, 1500, 1510, 0, 128, 0.02, (), False),
 ]
 
 
