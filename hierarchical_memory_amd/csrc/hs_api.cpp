@@ -813,7 +813,7 @@ int hs_attend_work_bytes(const hs_config* cfg, const hs_row_format* fmt, int32_t
     return fail(HS_E_INVALID, "rows of this format have %d bytes, the configuration's %d", row.bytes, cfg->row_bytes);
   rc = check_heads(heads);
   if (rc) return rc;
-  *bytes = hs::attend_work_bytes(cfg->num_requests, cfg->top_k, heads, row);
+  *bytes = hs::attend_work_bytes(hs::attend_plan(cfg->num_requests, cfg->top_k, heads, row), cfg->num_requests, heads, row);
   return ok();
 }
 
@@ -835,11 +835,11 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
   a.B = ctx->cfg.device_buffer_size;
   a.T = ctx->cfg.tail_tokens;
   a.heads = heads;
-  const uint64_t need = hs::attend_work_bytes(a.R, a.k, heads, a.row);
+  const hs::AttendPlan plan = hs::attend_plan(a.R, a.k, heads, a.row);
+  const uint64_t need = hs::attend_work_bytes(plan, a.R, heads, a.row);
   if (need > 0 && (!d_work || work_bytes < need))
     return fail(HS_E_INVALID, "work buffer has %llu bytes, needs %llu", (unsigned long long)(d_work ? work_bytes : 0),
                 (unsigned long long)need);
-  const hs::AttendPlan plan = hs::attend_plan(a.R, a.k, heads, a.row);
   a.groups = plan.groups;
   a.splits = plan.splits;
   a.scale = scale;
@@ -863,7 +863,7 @@ int hs_attend_prompt_work_bytes(int32_t num_requests, int32_t n_q, int32_t n_k, 
     return fail(HS_E_INVALID, "num_requests must be in [1, 65535] (got %d)", num_requests);
   const int rc = check_prompt(n_q, n_k, heads, nope, rope, value);
   if (rc) return rc;
-  *bytes = hs::prompt_work_bytes(num_requests, n_q, n_k, heads, value);
+  *bytes = hs::prompt_work_bytes(hs::prompt_plan(num_requests, n_q, n_k, heads, value), n_q, heads, value);
   return ok();
 }
 
@@ -884,7 +884,8 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
     return fail(HS_E_INVALID, "rope_stride must be a multiple of 8 and at least %d (got %lld)", rope, (long long)rope_stride);
   if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_rope, 16) || !aligned(d_o, 16) || !aligned(d_work, 16))
     return fail(HS_E_INVALID, "q, kv, rope, o and work must be 16-byte aligned");
-  const uint64_t need = hs::prompt_work_bytes(ctx->cfg.num_requests, n_q, n_k, heads, value);
+  const hs::PromptPlan plan = hs::prompt_plan(ctx->cfg.num_requests, n_q, n_k, heads, value);
+  const uint64_t need = hs::prompt_work_bytes(plan, n_q, heads, value);
   if (need > 0 && (!d_work || work_bytes < need))
     return fail(HS_E_INVALID, "work buffer has %llu bytes, needs %llu", (unsigned long long)(d_work ? work_bytes : 0),
                 (unsigned long long)need);
@@ -902,7 +903,6 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
   a.q = (const uint16_t*)d_q;
   a.kv = (const uint16_t*)d_kv;
   a.krope = (const uint16_t*)d_rope;
-  const hs::PromptPlan plan = hs::prompt_plan(a.R, n_q, n_k, heads, value);
   a.sets = plan.sets;
   a.splits = plan.splits;
   a.items = plan.items;

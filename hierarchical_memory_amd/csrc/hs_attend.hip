@@ -595,8 +595,8 @@ AttendPlan attend_plan(int R, int k, int heads, const RowLayout& row) {
   return best;
 }
 
-uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row) {
-  const uint64_t s = (uint64_t)attend_plan(R, k, heads, row).splits;
+uint64_t attend_work_bytes(const AttendPlan& plan, int R, int heads, const RowLayout& row) {
+  const uint64_t s = (uint64_t)plan.splits;
   return s == 1 ? 0 : (uint64_t)R * heads * s * (16 + 4ull * row.latent);
 }
 

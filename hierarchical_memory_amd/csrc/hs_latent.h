@@ -101,14 +101,14 @@ struct AttendPlan {
   int groups, splits;
 };
 AttendPlan attend_plan(int R, int k, int heads, const RowLayout& row);
-uint64_t attend_work_bytes(int R, int k, int heads, const RowLayout& row);
+uint64_t attend_work_bytes(const AttendPlan& plan, int R, int heads, const RowLayout& row);
 
 // The same for hs_attend_prompt.
 struct PromptPlan {
   int sets, splits, items;
 };
 PromptPlan prompt_plan(int R, int n_q, int n_k, int heads, int value);
-uint64_t prompt_work_bytes(int R, int n_q, int n_k, int heads, int value);
+uint64_t prompt_work_bytes(const PromptPlan& plan, int n_q, int heads, int value);
 
 // Allows the attention kernels the LDS that they take, on the current device.
 hipError_t set_attend_lds();

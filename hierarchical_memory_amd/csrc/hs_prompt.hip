@@ -632,8 +632,8 @@ PromptPlan prompt_plan(int R, int n_q, int n_k, int heads, int value) {
   return best;
 }
 
-uint64_t prompt_work_bytes(int R, int n_q, int n_k, int heads, int value) {
-  const uint64_t s = (uint64_t)prompt_plan(R, n_q, n_k, heads, value).splits;
+uint64_t prompt_work_bytes(const PromptPlan& plan, int n_q, int heads, int value) {
+  const uint64_t s = (uint64_t)plan.splits;
   return s == 1 ? 0 : (uint64_t)n_q * heads * s * (16 + 4ull * value);
 }
 
