@@ -4,8 +4,8 @@
 //   s = scale * q . row,   o = sum_j p_j latent_j / sum_j p_j,   p_j = 2^(s_j log2 e - m)   (m a running maximum)
 //
 // One pass over the rows, 32 to a tile. A workgroup of eight waves, two to a SIMD, takes a part of one request's selection
-// and up to 128 of its heads; it reads each row once, whatever the number of heads. Matrix instructions do both products
-// transposed, so that a head is a lane's column in both and its maximum, sum and rescaling stay inside four lanes:
+// and up to 128 of its heads, for all of which it reads a row once. Matrix instructions do both products transposed, so that a
+// head is a lane's column in both and its maximum, sum and rescaling stay inside four lanes:
 //   S^T[key][head]  = K Q^T     A: the tile's rows from LDS, B: the queries, kept in registers
 //   O^T[dim][head] += V^T P^T   A: the same rows read through the transposing LDS load, B: the weights as S^T left them
 // (lane group g = lane / 16 holds the keys 4 g + 0..3 and 16 + 4 g + 0..3 of S^T; the second product takes its keys in that
