@@ -261,6 +261,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     }
     return (uint32_t)__ballot(r.lane >= 0);
   };
+
   // LDS places of this lane's reads, but for the tile's start
   int kat[2], vat[4];
 #pragma unroll
