@@ -180,8 +180,9 @@ constexpr int kStoreWaves = kStoreThreads / 64;
 
 // One wave per token: a lane holds 8 latent values (16-byte loads and stores) and, below rope / 2, one pair of the rope
 // part. The 4 lanes of a scale block share its largest magnitude. Memory bounds it: 41 K tokens of 512 + 64 values, 141 MB, in
-// 31 us (4.5 TB/s, a copy reaches 4.8); 256 tokens in 3.8 us.
-__global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
+// 31 us (4.5 TB/s, a copy reaches 4.8); 256 tokens in 3.8 us. Seven waves to a SIMD (72 registers): with six the large call takes
+// 32.5 us.
+__global__ __launch_bounds__(kStoreThreads, 7) void store_kernel(StoreArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int L = a.row.latent, P = a.row.rope / 2;
   const bool has = lane * 8 < L, pair = lane < P;
@@ -223,7 +224,11 @@ __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
       for (int i = 0; i < 8; ++i) d += (double)y[i] * (double)y[i];
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) d += __shfl_xor(d, m);
-      inv = (float)(1.0 / sqrt(d / (double)L + (double)a.eps));
+      // (the inverse too may be past 32 bits, 1e40 for the least of bf16's subnormals: the values are lifted first, exactly)
+      const float lift = sq < 1.0f ? 0x1p40f : 0x1p-40f;
+      inv = (float)(1.0 / sqrt((d / (double)L + (double)a.eps) * ((double)lift * lift)));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= lift;
     }
     bf8 yb;
 #pragma unroll
