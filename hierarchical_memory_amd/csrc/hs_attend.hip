@@ -387,11 +387,11 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
     float top = s[0][0];
 #pragma unroll
     for (int i = 1; i < 4 * kKeyBlocks; ++i) top = fmaxf(top, s[i / 4][i % 4]);
-    top = max_of_quarters(top) * scale;
-    if (__any(top > m + kSlack)) {
+    top = max_of_quarters(top);
+    if (__any((top - m) * scale > kSlack)) {
       const float to = fmaxf(m, top);
       if (__any(m > -INFINITY)) {
-        const float c = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - to);
+        const float c = rebase(m, to, scale);
         sum *= c;
         rsum *= c;
 #pragma unroll
@@ -399,7 +399,13 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       }
       m = to;
     }
-    const float m0 = m == -INFINITY ? 0.0f : m;
+    float m0 = m == -INFINITY ? 0.0f : m * scale;
+    if (__any(fabsf(m0) >= kFar)) {
+      const bool apart = fabsf(m0) >= kFar;
+#pragma unroll
+      for (int i = 0; i < 4 * kKeyBlocks; ++i) s[i / 4][i % 4] -= apart ? m : 0.0f;
+      m0 = apart ? 0.0f : m0;
+    }
     bf8 p;
 #pragma unroll
     for (int i = 0; i < 4 * kKeyBlocks; i += 2) weigh_pair(s[i / 4][i % 4], s[i / 4][i % 4 + 1], scale, m0, p, i, sum, rsum);
@@ -439,9 +445,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
         given[(3 + 4 * b + j) * kStep] = key_half ? o[b][j] : o[kOut + b][j];
       }
     __syncthreads();
-    const float other = theirs[0], to = fmaxf(m, other);
-    const float c0 = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - to);
-    const float c1 = other == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(other - to);
+    const float other = theirs[0], to = fmaxf(m, other), c0 = rebase(m, to, scale), c1 = rebase(other, to, scale);
     m = to;
     sum = sum * c0 + theirs[kStep] * c1;
     rsum = rsum * c0 + theirs[2 * kStep] * c1;
@@ -467,7 +471,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
       *(bf4*)(dst + 16 * b) = v;
     }
     if (a.lse && wave % kShare == 0 && group == 0)
-      a.lse[rh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
+      a.lse[rh] = sum > 0.0f ? m * scale * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
     return;
   }
   // partial results: [R][heads][splits] of (m, sum, rsum, -) and [R][heads][splits][L]
@@ -505,7 +509,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   float m = max_of_quarters(v[0]);
 #pragma unroll
   for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const float c = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(v[0] - m);
+  const float scale = scale_of(a.scale), c = rebase(v[0], m, scale);
   float sum = c * v[1], rsum = c * v[2];
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -535,7 +539,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
     for (int i = 0; i < 4; ++i) r[i] = (__bf16)(all[i] * f);
     *(bf4*)((__bf16*)a.o + rh * L + 4 * d) = r;
   }
-  if (a.lse && threadIdx.x == 0) a.lse[rh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
+  if (a.lse && threadIdx.x == 0) a.lse[rh] = sum > 0.0f ? m * scale * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
 }
 
 template <int L, int P, bool kMx, int kGroups>

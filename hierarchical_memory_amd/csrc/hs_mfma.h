@@ -54,6 +54,24 @@ __device__ __forceinline__ bf8 turned(v4u x, uint32_t sign) {
 // The magnitude of the scale, to base 2. Not zero: a score that a mask took out, -infinity, stays so.
 __device__ __forceinline__ float scale_of(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1.17549435e-38f); }
 
+// The running maximum m is a score, unscaled, and weights are relative to m times the scale in 32 bits, which one fma takes off
+// a scaled score. Its rounding cancels, being the same for all of them, as long as it is small beside the exponents' range:
+// from kFar on (where it reaches one) a weight is that of the score's distance from m instead, which any two scores have
+// (2^(s scale - m scale) would end at 0 or infinity for the maximum itself from about 2^30 on).
+constexpr float kFar = 16777216.0f;
+__device__ __forceinline__ bool is_far(float m, float scale) { return fabsf(m * scale) >= kFar; }
+
+// What the product of m and the scale lost in rounding, where the weights are relative to it.
+__device__ __forceinline__ float rest_of(float m, float scale) {
+  return is_far(m, scale) ? 0.0f : fmaf(m, scale, -(m * scale));
+}
+
+// The factor that takes weights relative to the maximum `from` to those relative to `to` (zero from -infinity, no score yet).
+__device__ __forceinline__ float rebase(float from, float to, float scale) {
+  return from == -INFINITY ? 0.0f
+                           : __builtin_amdgcn_exp2f((from - to) * scale + (rest_of(to, scale) - rest_of(from, scale)));
+}
+
 // The weights 2^(s scale - m) of two of a lane's scores, rounded to bf16 in p[i] and p[i + 1] for the second product; their
 // sum is added to `sum`, that of the rounded ones, one dot product with ones, to `rsum`.
 __device__ __forceinline__ void weigh_pair(float s0, float s1, float scale, float m, bf8& p, int i, float& sum,

@@ -339,16 +339,16 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       bool any = false;
 #pragma unroll
       for (int g = 0; g < kSets; ++g) {
-        top[g] = max_of_halves(top[g]) * scale;
-        any |= top[g] > m[g] + kSlack;
+        top[g] = max_of_halves(top[g]);
+        any |= (top[g] - m[g]) * scale > kSlack;
       }
       return __any(any);
     };
     auto raise = [&]() {
 #pragma unroll
       for (int g = 0; g < kSets; ++g) {
-        const float to = top[g] > m[g] + kSlack ? top[g] : m[g];
-        const float c = m[g] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[g] - to);
+        const float to = (top[g] - m[g]) * scale > kSlack ? top[g] : m[g];
+        const float c = rebase(m[g], to, scale);
         if (__any(m[g] > -INFINITY && c != 1.0f)) {
           sum[g] *= c;
           rsum[g] *= c;
@@ -369,7 +369,19 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       bf8 p[kSets][2];
       float m0[kSets];
 #pragma unroll
-      for (int g = 0; g < kSets; ++g) m0[g] = m[g] == -INFINITY ? 0.0f : m[g];
+      for (int g = 0; g < kSets; ++g) m0[g] = m[g] == -INFINITY ? 0.0f : m[g] * scale;
+      bool any_far = false;
+#pragma unroll
+      for (int g = 0; g < kSets; ++g) any_far |= fabsf(m0[g]) >= kFar;
+      if (__any(any_far)) {
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) {
+          const bool far = fabsf(m0[g]) >= kFar;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[g][e] -= far ? m[g] : 0.0f;
+          m0[g] = far ? 0.0f : m0[g];
+        }
+      }
       constexpr int kReads = 3;  // blocks of values that are read before the products of the block before them end
       bf8 v[kReads][2];
       auto read_values = [&](int b) {
@@ -494,7 +506,7 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
             *(bf4*)(dst + 32 * b + 8 * c) = v;
           }
         if (a.lse && half == 0)
-          a.lse[qh] = sum[g] > 0.0f ? m[g] * kLn2 + logf(sum[g]) : sum[g] == 0.0f ? -INFINITY : sum[g];
+          a.lse[qh] = sum[g] > 0.0f ? m[g] * scale * kLn2 + logf(sum[g]) : sum[g] == 0.0f ? -INFINITY : sum[g];
         continue;
       }
       float* dst = a.work + (size_t)a.n_q * a.heads * a.splits * 4 + ph * DV + 4 * half;
@@ -535,6 +547,7 @@ template <int DV>
 __global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
   constexpr int kPer = DV / 64;
   const int lane = threadIdx.x & 63;
+  const float scale = scale_of(a.scale);
   // rows before the first sequence and behind the last have no parts
   const size_t n0 = (size_t)cut(a.cu_q[0], a.n_q) * a.heads, n = (size_t)cut(a.cu_q[a.R], a.n_q) * a.heads;
   for (size_t qh = n0 + (size_t)blockIdx.x * 4 + (threadIdx.x >> 6); qh < n; qh += (size_t)gridDim.x * 4) {
@@ -544,12 +557,11 @@ __global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
     if (parts == 1) continue;
     float m = -INFINITY;
     for (int s = 0; s < parts; ++s) m = fmaxf(m, st[s][0]);
-    const float m0 = m == -INFINITY ? 0.0f : m;
     float sum = 0.0f, rsum = 0.0f, o[kPer] = {};
     const float* src = a.work + (size_t)a.n_q * a.heads * a.splits * 4 + qh * a.splits * DV + lane * kPer;
     for (int s = 0; s < parts; ++s) {
       const f4 v = st[s];
-      const float c = __builtin_amdgcn_exp2f(v[0] - m0);
+      const float c = rebase(v[0], m, scale);
       sum += c * v[1];
       rsum += c * v[2];
 #pragma unroll
@@ -559,7 +571,7 @@ __global__ __launch_bounds__(256) void join_prompt_kernel(PromptArgs a) {
     __bf16* dst = (__bf16*)a.o + qh * DV + lane * kPer;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) dst[i] = (__bf16)(o[i] * f);
-    if (a.lse && lane == 0) a.lse[qh] = sum > 0.0f ? m * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
+    if (a.lse && lane == 0) a.lse[qh] = sum > 0.0f ? m * scale * kLn2 + logf(sum) : sum == 0.0f ? -INFINITY : sum;
   }
 }
 

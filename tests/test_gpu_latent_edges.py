@@ -20,7 +20,7 @@ def _gpu():
 
 import hierarchical_memory_amd as hm  # noqa: E402
 from tests import latent_ref as ref  # noqa: E402
-from tests.test_gpu_latent import _check_row  # noqa: E402
+from tests.test_gpu_latent import Attend, _check_row, _cu, _within  # noqa: E402
 
 
 # ---- store
@@ -47,4 +47,99 @@ def test_store_norm_at_the_ends_of_bf16(unit, eps, mx):
                      (1 + torch.arange(n)).to(torch.int32).cuda(), lat)
     for t in range(n):
         _check_row(sw.tail[0, t].cpu(), lat[t].cpu(), x[t], w, eps, t, None, False, latent, rope, mx, f"token {t}")
+    sw.close()
+
+
+# ---- scores of any size
+
+# Queries and keys of small whole numbers: every score is a whole number below 2^24 and so exact in 32 bits, times the power
+# of two of its head. What is left is the rounding of a weight's exponent, relative to the exponent: under 40 nats of distance
+# (weights below e^-40 are nothing), 40 * 8 half steps of 32 bits.
+EXACT_SCORE_ERROR = 40 * 8 * ref.F32_HALF
+
+
+# A far lse is the maximum times scale and log2 e, and back by ln 2: six roundings (both constants, three products, the sum of the
+# logarithm), where attention_bounds counts four (an ordinary score's own error covers the others).
+MORE_OF_LSE = 2 * ref.F32_HALF
+
+
+def _nothing(keys):
+    """What weights that end at zero may add: each is below 2^-126 of the largest (the least normal number), the largest is
+    part of the sum, and values are 3 at most."""
+    return keys * 3 * 2.0 ** -126
+
+
+def _whole(shape, gen, most=3):
+    return torch.randint(-most, most + 1, shape, generator=gen).to(torch.float32).bfloat16()
+
+
+def _whole_rows(shape, latent, rope, mx, gen):
+    v = _whole((*shape, latent + rope), gen)
+    if not mx:
+        return v.view(torch.uint8)
+    s, at, _ = ref.row_layout(latent, rope, True)
+    e4m3 = v[..., :latent].float().to(torch.float8_e4m3fn).view(torch.uint8)
+    scales = torch.full((*shape, at - s), 127, dtype=torch.uint8)
+    return torch.cat([e4m3, scales, v[..., latent:].contiguous().view(torch.uint8)], -1)
+
+
+def _powers(heads, gen):
+    """A power of two for each head, from scores of about one to 2^100, in no order."""
+    return torch.exp2((100 * torch.arange(heads) // max(heads - 1, 1))[torch.randperm(heads, generator=gen)].double())
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("R,k,heads,latent,rope", [(2, 40, 16, 512, 64), (1, 700, 100, 512, 64), (2, 300, 24, 256, 32),
+                                                   (200, 90, 60, 512, 64), (180, 57, 128, 512, 64)])
+def test_attend_scores_of_any_size(R, k, heads, latent, rope, mx, sign):
+    """Heads whose scores reach from about one to 2^107: far ones take the row of the largest score (rows of one score share),
+    near ones are as ever."""
+    c = Attend(R, k, k + 5, 0, heads, latent, rope, mx, seed=50, pad=0.05)
+    gen = torch.Generator().manual_seed(51)
+    c.rows = _whole_rows((R, k + 5), latent, rope, mx, gen)
+    c.sw.hot.copy_(c.rows)
+    c.q = (_whole((R, heads, latent + rope), gen).double() * _powers(heads, gen)[:, None]).bfloat16()
+    c.dev["q"] = c.q.cuda()
+    c.scale = sign * 2.0 ** -7
+    c.run()
+    for r in {0, R // 2, R - 1}:
+        rows = ref.unpack(c.rows[r][c.out[r][c.out[r] >= 0].long()], latent, rope, mx)
+        # (weights over their own sum: beside 2^53 a logarithm would lose that equal scores share)
+        s = c.q[r].double() @ rows.T * c.scale
+        p, lse = torch.softmax(s, 1), torch.logsumexp(s, 1)
+        o, pv = p @ rows[:, :latent], p @ rows[:, :latent].abs()
+        bo, bl = ref.attention_bounds(o, lse, pv, torch.full((heads,), EXACT_SCORE_ERROR, dtype=torch.float64), rows.shape[0])
+        _within(c.o[r], o, bo + _nothing(rows.shape[0]), f"request {r} o")
+        _within(c.lse[r], lse, bl + MORE_OF_LSE * lse.abs(), f"request {r} lse")
+    c.close()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("nope,rope,value", [(64, 32, 64), (128, 64, 128), (192, 64, 256)])
+@pytest.mark.parametrize("nq,nk,heads", [([40, 3], [40, 300], 8), ([1], [5000], 4), ([40, 3, 0], [2600, 1400, 900], 2),
+                                         ([200], [200], 512), ([130], [4130], 64)])
+def test_prompt_scores_of_any_size(nq, nk, heads, nope, rope, value, sign):
+    gen = torch.Generator().manual_seed(52)
+    sw = hm.SwapIn(hm.config(len(nq), 1, 1, 0.0, 16, 4, 0))
+    N, M = sum(nq), sum(nk)
+    q = (_whole((N, heads, nope + rope), gen).double() * _powers(heads, gen)[:, None]).bfloat16()
+    kv, kr = _whole((M, heads, nope + value), gen), _whole((M, rope), gen)
+    o = torch.full((N, heads, value), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N, heads), 9.0, device="cuda")
+    scale = sign * 2.0 ** -6
+    cu_q, cu_k = _cu(nq), _cu(nk)
+    hm.hs_attend_prompt(sw.ctx, q.cuda(), kv.cuda(), kr.cuda(), cu_q.cuda(), cu_k.cuda(), scale, o, lse)
+    for r in range(len(nq)):
+        a, b, c, d = int(cu_q[r]), int(cu_q[r + 1]), int(cu_k[r]), int(cu_k[r + 1])
+        for h in range(0, heads, max(1, heads // 8)):
+            n = d - c
+            seen = torch.arange(n)[None, :] <= (n - (b - a)) + torch.arange(b - a)[:, None]
+            s = q[a:b, h].double() @ torch.cat([kv[c:d, h, :nope], kr[c:d]], 1).double().T * scale
+            s = s.masked_fill(~seen, -torch.inf)
+            p, lse_want, v = torch.softmax(s, 1), torch.logsumexp(s, 1), kv[c:d, h, nope:].double()
+            bo, bl = ref.attention_bounds(p @ v, lse_want, p @ v.abs(),
+                                          torch.full((b - a,), EXACT_SCORE_ERROR, dtype=torch.float64), n)
+            _within(o[a:b, h], p @ v, bo + _nothing(n), f"sequence {r} head {h} o")
+            _within(lse[a:b, h], lse_want, bl + MORE_OF_LSE * lse_want.abs(), f"sequence {r} head {h} lse")
     sw.close()
