@@ -826,7 +826,7 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
   if (rc) return rc;
   rc = check_heads(heads);
   if (rc) return rc;
-  if (!std::isfinite(scale)) return fail(HS_E_INVALID, "scale must be finite");
+  if (!(std::fabs(scale) < 0x1p127f)) return fail(HS_E_INVALID, "scale must be finite and below 2^127 (got %g)", (double)scale);
   if (!d_q || !d_out || !d_o) return fail(HS_E_INVALID, "q, out and o must not be NULL");
   if (!aligned(d_q, 16) || !aligned(d_o, 16) || !aligned(d_gather, 16) || !aligned(d_work, 16))
     return fail(HS_E_INVALID, "q, o, gather and work must be 16-byte aligned");
@@ -875,7 +875,7 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
   if (rc) return rc;
   rc = check_prompt(n_q, n_k, heads, nope, rope, value);
   if (rc) return rc;
-  if (!std::isfinite(scale)) return fail(HS_E_INVALID, "scale must be finite");
+  if (!(std::fabs(scale) < 0x1p127f)) return fail(HS_E_INVALID, "scale must be finite and below 2^127 (got %g)", (double)scale);
   if (causal != 0 && causal != 1) return fail(HS_E_INVALID, "causal must be 0 or 1 (got %d)", causal);
   if (!d_cu_q || !d_cu_k) return fail(HS_E_INVALID, "cu_q and cu_k must not be NULL");
   if (n_q > 0 && (!d_q || !d_o)) return fail(HS_E_INVALID, "q and o must not be NULL");

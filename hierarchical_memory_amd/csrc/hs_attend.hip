@@ -298,6 +298,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
 #pragma unroll
     for (int i = 0; i < S::kSteps; ++i)
       q[i] = turned(*(const v4u*)(tile + kat[i & 1] + S::kColBytes * (i >> 1)), sign);
+    if (a.scale == 0.0f) zero_scaled(q);
 #pragma unroll
     for (int i = 0; i < S::kSteps; ++i) asm volatile("" : "+v"(q[i]));  // read, before others write there
     asm volatile("s_barrier" ::: "memory");

@@ -51,8 +51,18 @@ __device__ __forceinline__ bf8 turned(v4u x, uint32_t sign) {
   return __builtin_bit_cast(bf8, x);
 }
 
-// The magnitude of the scale, to base 2. Not zero: a score that a mask took out, -infinity, stays so.
-__device__ __forceinline__ float scale_of(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1.17549435e-38f); }
+// A scale of zero is applied to the queries: as a factor of scores it would make a masked one, -infinity, NaN.
+template <int kN>
+__device__ __forceinline__ void zero_scaled(bf8 (&q)[kN]) {
+#pragma unroll
+  for (int s = 0; s < kN; ++s)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)((float)q[s][i] * 0.0f);
+}
+
+// The magnitude of the scale, to base 2, for such queries. (Below 2^-126 it has fewer digits; what that changes of an exponent
+// is less than 2^-22.)
+__device__ __forceinline__ float scale_of(float scale) { return scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e; }
 
 // The running maximum m is a score, unscaled, and weights are relative to m times the scale in 32 bits, which one fma takes off
 // a scaled score. Its rounding cancels, being the same for all of them, as long as it is small beside the exponents' range:

@@ -259,6 +259,7 @@ __global__ __launch_bounds__((PromptShape<DN, P, DV, kSets>::kThreads)) void pro
       for (int s = 0; s < S::kSteps; ++s) {
         q[g][s] = turned(*(const v4u*)(src + 16 * s), sign);
       }
+      if (a.scale == 0.0f) zero_scaled(q[g]);
     }
 #pragma unroll
     for (int g = 0; g < kSets; ++g)

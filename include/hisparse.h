@@ -407,8 +407,8 @@ int hs_store_rows(hs_ctx* ctx, const hs_row_format* fmt, const void* d_x, int64_
  *             one each. Nothing in it has to start at zero.
  * Scores, sums and partial results are held in 32 bits; the softmax weights are rounded to bf16 for the product with the
  * rows (the sum that divides it is that of the rounded weights), the result once to bf16. The order of every sum is fixed,
- * so equal inputs give equal bits. scale must be finite; q_h . v_j may be of any size that 32 bits hold. Rows that are not
- * selected are not read, so nothing in them reaches the result.
+ * so equal inputs give equal bits. |scale| must be below 2^127; q_h . v_j may be of any size that 32 bits hold. Rows that
+ * are not selected are not read, so nothing in them reaches the result.
  */
 int hs_attend_work_bytes(const hs_config* cfg, const hs_row_format* fmt, int32_t heads, uint64_t* bytes);
 int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t heads, float scale, const int32_t* d_out,

@@ -143,3 +143,45 @@ def test_prompt_scores_of_any_size(nq, nk, heads, nope, rope, value, sign):
             _within(o[a:b, h], p @ v, bo + _nothing(n), f"sequence {r} head {h} o")
             _within(lse[a:b, h], lse_want, bl + MORE_OF_LSE * lse_want.abs(), f"sequence {r} head {h} lse")
     sw.close()
+
+
+# ---- scales
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 2.0 ** -128, -2.0 ** -133, 2.0 ** -149])
+@pytest.mark.parametrize("R,k,heads", [(2, 300, 24), (1, 700, 100), (180, 57, 128)])
+def test_attend_scales_that_vanish(R, k, heads, scale):
+    """A scale of zero beside scores near the largest number, and subnormal scales that such scores make matter."""
+    c = Attend(R, k, k + 5, 0, heads, 512, 64, False, seed=53, pad=0.05)
+    gen = torch.Generator().manual_seed(54)
+    c.rows = (torch.randn(R, k + 5, 576, generator=gen) * 2.0 ** 58).bfloat16().view(torch.uint8)
+    c.sw.hot.copy_(c.rows)
+    c.q = (torch.randn(R, heads, 576, generator=gen) * 2.0 ** 60).bfloat16()
+    c.dev["q"] = c.q.cuda()
+    c.scale = scale
+    c.run().check({0, R - 1})
+    for refused in (2.0 ** 127, -2.0 ** 127):  # times log2 e past 32 bits
+        c.scale = refused
+        with pytest.raises(hm.HiSparseError, match="2\\^127"):
+            c.run()
+    c.close()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 2.0 ** -128, -2.0 ** -133, 2.0 ** -149])
+@pytest.mark.parametrize("nq,nk,heads", [([40, 3], [40, 300], 8), ([3], [5000], 4), ([200], [200], 512)])
+def test_prompt_scales_that_vanish(nq, nk, heads, scale):
+    gen = torch.Generator().manual_seed(55)
+    sw = hm.SwapIn(hm.config(len(nq), 1, 1, 0.0, 16, 4, 0))
+    N, M = sum(nq), sum(nk)
+    q = (torch.randn(N, heads, 192, generator=gen) * 2.0 ** 60).bfloat16()
+    kv, kr = ((torch.randn(M, *s, generator=gen) * 2.0 ** 58).bfloat16() for s in ((heads, 256), (64,)))
+    o = torch.full((N, heads, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N, heads), 9.0, device="cuda")
+    cu_q, cu_k = _cu(nq), _cu(nk)
+    hm.hs_attend_prompt(sw.ctx, q.cuda(), kv.cuda(), kr.cuda(), cu_q.cuda(), cu_k.cuda(), scale, o, lse)
+    for r in range(len(nq)):
+        a, b, c, d = int(cu_q[r]), int(cu_q[r + 1]), int(cu_k[r]), int(cu_k[r + 1])
+        for h in range(0, heads, max(1, heads // 8)):
+            w = ref.prompt(q[a:b, h].double(), kv[c:d, h].double(), kr[c:d].double(), 128, scale, True)
+            _within(o[a:b, h], w[0], w[2], f"sequence {r} head {h} o")
+            _within(lse[a:b, h], w[1], w[3], f"sequence {r} head {h} lse")
+    sw.close()
