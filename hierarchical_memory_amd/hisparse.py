@@ -264,7 +264,8 @@ def _torch_stream(stream):
     if stream is None or not isinstance(stream, int):
         return stream
     import torch
-    return torch.cuda.ExternalStream(stream)
+    # (0 is the default stream; an ExternalStream of it would be a stream of torch's pool)
+    return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
 
 
 def _ptrs(*tensors):

@@ -185,3 +185,34 @@ def test_prompt_scales_that_vanish(nq, nk, heads, scale):
             _within(o[a:b, h], w[0], w[2], f"sequence {r} head {h} o")
             _within(lse[a:b, h], w[1], w[3], f"sequence {r} head {h} lse")
     sw.close()
+
+
+# ---- streams
+
+def test_prompt_work_buffer_on_the_default_stream_by_address(monkeypatch):
+    """The default stream's address is 0: the work buffer is taken on it, not on a stream of torch's pool."""
+    nq, nk, heads = [40, 3, 0], [2600, 1400, 900], 2
+    assert hm.hs_attend_prompt_work_bytes(3, 43, 4900, heads, 128, 64, 128) > 0
+    gen = torch.Generator().manual_seed(56)
+    sw = hm.SwapIn(hm.config(3, 1, 1, 0.0, 16, 4, 0))
+    q, kv, kr = (torch.randn(*s, generator=gen).bfloat16().cuda() for s in ((43, heads, 192), (4900, heads, 256), (4900, 64)))
+    o = [torch.full((43, heads, 128), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cu_q, cu_k = _cu(nq).cuda(), _cu(nk).cuda()
+    assert torch.cuda.default_stream().cuda_stream == 0
+    taken, empty = [], torch.empty
+
+    def watched(*a, **kw):
+        taken.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+
+    hm.hs_attend_prompt(sw.ctx, q, kv, kr, cu_q, cu_k, 0.07, o[0])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        monkeypatch.setattr(torch, "empty", watched)
+        hm.hs_attend_prompt(sw.ctx, q, kv, kr, cu_q, cu_k, 0.07, o[1], stream=0)
+        monkeypatch.setattr(torch, "empty", empty)
+    torch.cuda.synchronize()
+    assert taken == [0]
+    assert torch.equal(o[0], o[1])
+    sw.close()

@@ -127,3 +127,19 @@ def test_prompt_arguments(fake_ctx):
                     (dict(), "GPU tensor")):
         with pytest.raises(ValueError, match=msg):
             hm.hs_attend_prompt(fake_ctx, **dict(good, **kw))
+
+
+def test_stream_of_an_address(monkeypatch):
+    """A work buffer is taken on the stream that the kernels run on: address 0 is the default stream."""
+    class External:
+        def __init__(self, address):
+            assert address, "torch takes a null address for none given"
+            self.cuda_stream = address
+
+    default = object()
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: default)
+    assert hm.hisparse._torch_stream(0) is default
+    assert hm.hisparse._torch_stream(0x1000).cuda_stream == 0x1000
+    assert hm.hisparse._torch_stream(None) is None
+    assert hm.hisparse._torch_stream(default) is default
