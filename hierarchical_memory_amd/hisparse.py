@@ -452,6 +452,8 @@ def hs_map_tokens(ctx, new, length, tail0, cu, req, pos, slot, status=None, stre
     lim = _CTX_SIZES.get(_ctx_key(ctx))
     R = lim.R if lim is not None else 0
     n = req.numel() if req is not None else 0
+    if n > 1 << 30:  # (as an int32 argument a length past 32 bits would wrap into one that the library takes)
+        raise ValueError(f"req, pos and slot must have at most {1 << 30} elements, got {n}")
     dev = new.get_device() if new is not None else -1
     if not (_i32_fine(new, R, dev) and _i32_fine(length, R, dev) and _i32_fine(cu, R + 1, dev)
             and _i32_fine(req, n, dev) and _i32_fine(pos, n, dev) and _i32_fine(slot, n, dev)

@@ -96,6 +96,14 @@ def test_map_arguments(fake_ctx):
             hm.hs_map_tokens(fake_ctx, **dict(good, **kw))
 
 
+@pytest.mark.parametrize("n", [(1 << 30) + 1, 1 << 31, (1 << 32) + 5])
+def test_map_length_past_the_limit(fake_ctx, n):
+    """Refused by the tensors' length, also where 32 bits of it would be a length in range."""
+    far = torch.empty(n, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="at most 1073741824"):
+        hm.hs_map_tokens(fake_ctx, _i32(3), _i32(3), _i32(3), _i32(4), far, far, far)
+
+
 def test_store_arguments(fake_ctx):
     good = dict(fmt=hm.row_format(), x=_bf(5, 576), weight=_bf(512), eps=1e-6, freqs=torch.zeros(32, dtype=torch.float64),
                 req=_i32(5), pos=_i32(5), slot=_i32(5), latent=_bf(5, 576))
