@@ -330,8 +330,10 @@ int hs_rebuild_order(hs_ctx* ctx, void* stream);
  * Row formats. latent is 256 or 512, rope 32 or 64:
  *   HS_ROW_BF16   [latent bf16][rope bf16]
  *   HS_ROW_MXFP8  [latent e4m3][latent / 32 scales e8m0, filled up to 16 bytes][rope bf16]: a latent value is its
- *                 e4m3 value times 2^(b - 127), b the scale byte of its block of 32 (1 .. 254). A power-of-two
- *                 scale keeps every value exact in bf16; it lies in the row because rows move one by one.
+ *                 e4m3 value times 2^(b - 127), b the scale byte of its block of 32. A power-of-two scale keeps
+ *                 every value exact in bf16, which the attention reads it as, for b from 10 (2^-9 becomes bf16's
+ *                 least normal number) to 246 (448 * 2^119); hs_store_rows writes 27 and up, past 246 only for
+ *                 values past 448 * 2^119. The scale lies in the row because rows move one by one.
  * The context's row_bytes must be hs_row_bytes of the format (1152 for 512 + 64 bf16 values, 656 in 8 bits).
  */
 #define HS_ROW_BF16 0
@@ -407,8 +409,9 @@ int hs_store_rows(hs_ctx* ctx, const hs_row_format* fmt, const void* d_x, int64_
  *             one each. Nothing in it has to start at zero.
  * Scores, sums and partial results are held in 32 bits; the softmax weights are rounded to bf16 for the product with the
  * rows (the sum that divides it is that of the rounded weights), the result once to bf16. The order of every sum is fixed,
- * so equal inputs give equal bits. |scale| must be below 2^127; q_h . v_j may be of any size that 32 bits hold. Rows that
- * are not selected are not read, so nothing in them reaches the result.
+ * so equal inputs give equal bits. |scale| must be below 2^127; q_h . v_j may be of any size that 32 bits hold. Latent
+ * values up to 2^80 in magnitude never make a sum overflow; the weights in it reach 2^16. Rows that are not selected are
+ * not read, so nothing in them reaches the result.
  */
 int hs_attend_work_bytes(const hs_config* cfg, const hs_row_format* fmt, int32_t heads, uint64_t* bytes);
 int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t heads, float scale, const int32_t* d_out,
@@ -431,7 +434,7 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
  *   d_work  hs_attend_prompt_work_bytes bytes of device memory, as in hs_attend (few queries over many keys are shared out
  *           over the keys too, and joined)
  * heads: 1 .. 512; (nope, value) one of (64, 64), (128, 128), (192, 256); rope 32 or 64; n_q, n_k from 0 to 2^30.
- * Precision as in hs_attend. An infinite value or a NaN in a key or value row reaches only the queries that see the row.
+ * Precision and ranges as in hs_attend. An infinite value or a NaN in a key or value row reaches only the queries that see the row.
  */
 int hs_attend_prompt_work_bytes(int32_t num_requests, int32_t n_q, int32_t n_k, int32_t heads, int32_t nope, int32_t rope,
                                 int32_t value, uint64_t* bytes);

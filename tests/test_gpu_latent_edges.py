@@ -187,6 +187,49 @@ def test_prompt_scales_that_vanish(nq, nk, heads, scale):
     sw.close()
 
 
+# ---- 8-bit rows
+
+def _scaled_rows(R, n, latent, rope, byte, gen):
+    """8-bit rows of every e4m3 number (both zeros, subnormals, 448), under one scale byte."""
+    numbers = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], dtype=torch.uint8)
+    s, at, _ = ref.row_layout(latent, rope, True)
+    q = numbers[torch.randint(0, len(numbers), (R, n, latent), generator=gen)]
+    scales = torch.full((R, n, at - s), byte, dtype=torch.uint8)
+    r = torch.randn(R, n, rope, generator=gen).bfloat16().view(torch.uint8)
+    return torch.cat([q, scales, r], -1)
+
+
+@pytest.mark.parametrize("byte", [10, 27, 127, 198, 246])
+@pytest.mark.parametrize("latent,rope", [(512, 64), (256, 32)])
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_attend_scale_bytes_are_exact(byte, latent, rope, heads):
+    """Attention over one row gives the row: every value of it exactly, at both ends of the range of scales."""
+    R = 200 if heads > 16 else 3  # enough that a workgroup takes all heads
+    c = Attend(R, 1, 2, 0, heads, latent, rope, True, seed=57)
+    c.rows = _scaled_rows(R, 2, latent, rope, byte, torch.Generator().manual_seed(byte))
+    c.sw.hot.copy_(c.rows)
+    c.q.zero_()
+    c.dev["q"] = c.q.cuda()
+    c.run()
+    rows = ref.unpack(c.rows, latent, rope, True)[torch.arange(R), c.out[:, 0].long(), :latent]
+    assert torch.equal(c.o.cpu().double(), rows[:, None].expand(R, heads, latent))
+    assert not c.lse.any()
+    c.close()
+
+
+@pytest.mark.parametrize("byte", [10, 198])
+@pytest.mark.parametrize("R,k,heads", [(2, 300, 24), (1, 700, 100), (180, 57, 128)])
+def test_attend_scale_bytes(byte, R, k, heads):
+    """Many rows, whose values reach 2^-126 and 2^80."""
+    c = Attend(R, k, k + 5, 0, heads, 512, 64, True, seed=58, pad=0.05)
+    gen = torch.Generator().manual_seed(59)
+    c.rows = _scaled_rows(R, k + 5, 512, 64, byte, gen)
+    c.sw.hot.copy_(c.rows)
+    c.q[..., :512] = (torch.randn(R, heads, 512, generator=gen) * 2.0 ** (127 - byte - 7)).bfloat16()
+    c.dev["q"] = c.q.cuda()
+    c.run().check({0, R - 1}).close()
+
+
 # ---- streams
 
 def test_prompt_work_buffer_on_the_default_stream_by_address(monkeypatch):
