@@ -424,9 +424,9 @@ int hs_attend(hs_ctx* ctx, const hs_row_format* fmt, const void* d_q, int32_t he
  * product leaves it, and the rope part, shared by all heads, is read from the latent rows themselves.
  *   d_q     [n_q][heads][nope + rope] bf16;  d_kv [n_k][heads][nope + value] bf16;  both 16-byte aligned
  *   d_rope  rope values of key token j at d_rope + j * rope_stride elements (16-byte aligned, stride a multiple of 8)
- *   d_cu_q, d_cu_k  [R + 1] starts of each request's queries and keys, ascending from 0 (values are cut to
- *           [0, n_q] and [0, n_k]; a request whose end lies before its start has none; a query row that two requests
- *           name has no defined result)
+ *   d_cu_q, d_cu_k  [R + 1] starts of each request's queries and keys, ascending from 0. Whatever they hold, nothing
+ *           outside the tensors is touched: values are cut to [0, n_q] and [0, n_k], and a request whose end lies before
+ *           its start has none. Where cu_q descends, or two requests name a query row, o and lse have no defined result
  *   causal  1: query i of a request with m queries and n keys sees its first n - m + i + 1 keys (the queries are the last
  *           m tokens); 0: all n
  *   d_o     [n_q][heads][value] bf16, 16-byte aligned;  d_lse [n_q][heads] float32 or NULL. Zeros and -inf for a query

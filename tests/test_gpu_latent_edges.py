@@ -259,3 +259,63 @@ def test_prompt_work_buffer_on_the_default_stream_by_address(monkeypatch):
     assert taken == [0]
     assert torch.equal(o[0], o[1])
     sw.close()
+
+
+# ---- boundaries that no batch has
+
+class Guarded:
+    """A tensor inside a larger allocation whose other bytes have to stay as they are."""
+    PAD = 1 << 16
+
+    def __init__(self, shape, dtype, fill):
+        n = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+        n += -n % 16
+        self.whole = (torch.arange(n + 2 * self.PAD, device="cuda") % 251).to(torch.uint8)
+        self.before = self.whole.clone()
+        inner = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+        self.t = self.whole[self.PAD:self.PAD + inner].view(dtype).view(shape)
+        self.t.fill_(fill)
+        self.inner = inner
+
+    def kept(self):
+        a, b = self.PAD, self.PAD + self.inner
+        return torch.equal(self.whole[:a], self.before[:a]) and torch.equal(self.whole[b:], self.before[b:])
+
+
+@pytest.mark.parametrize("nope,rope,value,n_q,n_k,heads", [(128, 64, 128, 66, 60, 2), (128, 64, 128, 60, 5000, 2),
+                                                           (192, 32, 256, 60, 5000, 2), (64, 32, 64, 60, 3000, 1),
+                                                           (128, 32, 128, 300, 300, 300)])
+@pytest.mark.parametrize("fault", ["past the end", "below zero", "descending", "all of them"])
+def test_prompt_bad_boundaries_write_only_their_tensors(fault, nope, rope, value, n_q, n_k, heads):
+    """Starts out of range or descending: o, lse and the work buffer are written inside only, and where the starts of the
+    queries, cut to the tensor, ascend, results are right."""
+    big, least = 2**31 - 1, -2**31
+    cu_q, cu_k, sound = {
+        # (sound: the request whose rows no other names, and its rows and keys)
+        "past the end": ([0, 20, 40, big], [0, 30, n_k // 2, big], (1, 20, 40, 30, n_k // 2)),
+        "below zero": ([least, 25, 50, 50], [-7, 20, n_k, n_k], (1, 25, 50, 20, n_k)),
+        "descending": ([0, 30, 10, 10], [0, n_k, 10, 10], None),
+        "all of them": ([-3, big, 5, least], [least, big, least, big], None),
+    }[fault]
+    gen = torch.Generator().manual_seed(60)
+    sw = hm.SwapIn(hm.config(3, 1, 1, 0.0, 16, 4, 0))
+    q = torch.randn(n_q, heads, nope + rope, generator=gen).bfloat16()
+    kv, kr = torch.randn(n_k, heads, nope + value, generator=gen).bfloat16(), torch.randn(n_k, rope, generator=gen).bfloat16()
+    o, lse = Guarded((n_q, heads, value), torch.bfloat16, 9.0), Guarded((n_q, heads), torch.float32, 9.0)
+    work = Guarded((hm.hs_attend_prompt_work_bytes(3, n_q, n_k, heads, nope, rope, value),), torch.uint8, 0xFF)
+    args = (q.cuda(), kv.cuda(), kr.cuda(), torch.tensor(cu_q, dtype=torch.int32, device="cuda"),
+            torch.tensor(cu_k, dtype=torch.int32, device="cuda"), 0.07)
+    for causal in (True, False):
+        o.t.fill_(9.0)
+        lse.t.fill_(9.0)
+        hm.hs_attend_prompt(sw.ctx, *args, o.t, lse.t, causal, work=work.t if work.t.numel() else None)
+        torch.cuda.synchronize()
+        assert o.kept() and lse.kept() and work.kept()
+        if sound is None:
+            continue
+        r, a, b, c, d = sound
+        for h in {0, heads - 1}:
+            w = ref.prompt(q[a:b, h].double(), kv[c:d, h].double(), kr[c:d].double(), nope, 0.07, causal)
+            _within(o.t[a:b, h], w[0], w[2], f"{fault} head {h} o")
+            _within(lse.t[a:b, h], w[1], w[3], f"{fault} head {h} lse")
+    sw.close()
