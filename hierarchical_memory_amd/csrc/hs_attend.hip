@@ -12,10 +12,12 @@
 // order, so the weights never change lanes). With fewer than eight groups of 16 heads a group has more than one wave: half
 // of them take the first 16 keys of each tile, half the others (joined through LDS at the end), and the waves of a half share
 // out the latent dimensions of the second product and repeat the first. LDS reads bound it there: with all 32 keys to each
-// wave 256 requests x 2048 rows take 130 us for 16 heads and 146 for 64, with halves 112 and 127 (5.5 and 5.0 TB/s of rows,
-// what memory gives); 64 heads of 8-bit rows 152 and 133. With 128 heads 172 us (3.9 TB/s, 850 TFLOP/s): a tile's loads alone
-// take 130, and the two products' dependence and the waves' meeting at each tile keep them from hiding all of the rest.
-// 8-bit rows are converted to bf16 tiles, so their products cost the same, and what they spare in bytes shows only in part.
+// wave 256 requests x 2048 rows took 130 us for 16 heads and 146 for 64, with halves they take 111 and 124 (604 MB of rows at
+// 5.4 and 4.9 TB/s, what memory gives). With 128 heads 170 to 177 us by the card (3.5 TB/s of rows, 850 TFLOP/s): a tile's
+// loads alone take 130, and the two products' dependence and the waves' meeting at each tile keep them from hiding all of the
+// rest. 8-bit rows are converted to bf16 tiles, so their products cost the same, and a tile passes LDS four times (in, out to be
+// converted, in, out to the products): of the bytes that they spare almost nothing shows, 102, 111, 130 and 181 us for 16, 32,
+// 64 and 128 heads where bf16 rows take 111, 115, 124 and 171.
 #include "hs_latent.h"
 #include "hs_mfma.h"
 
@@ -486,7 +488,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
 
 // Joins the parts of one request and head: a workgroup of four waves takes both, each wave every fourth part (all of a wave's
 // parts on their way at once), and the waves' sums are added in their order. 32 requests x 16 heads x 8 parts, 8 MB, take
-// 4.8 us, 64 x 64 x 4 parts, 34 MB, 8.8.
+// 4.0 us, 64 x 64 x 4 parts, 34 MB, 8.4.
 template <int L>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   constexpr int kPer = L / 64, kOnWay = 4;

@@ -29,7 +29,8 @@ __device__ __forceinline__ void wait_loads_and_meet() {
 }
 
 // 16 bytes of each lane's address + kOffset to LDS at lds + 16 * lane (the instruction adds its offset to both). It takes the LDS
-// address from m0, a register that the compiler sets right before each use of its own and keeps nothing in.
+// address from m0, a register that is reserved: the compiler keeps nothing in it (a clobber list may not name it), and no other
+// instruction of these kernels uses it.
 template <int kOffset>
 __device__ __forceinline__ void load_to_lds(const char* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds - kOffset), "v"(p),

@@ -12,11 +12,14 @@
 // There are only one or two waves to a SIMD, so the two pipes are kept busy from within a wave: a step of 32 keys computes the
 // next step's scores between the exponentials of its own, and takes their maximum between its products with the values.
 //
-// What bounds it: the matrix units and the card's power. 8192 tokens x 16 heads (128 + 64 / 128 values, causal) take 350 to
-// 385 us on different cards, 980 to 890 TFLOP/s, where a plain matrix product of the library reaches 1200; with
-// 32 queries to a wave they take 414 (twice the LDS reads for a product). 256 values allow only 32: 4
-// chunks of 512 tokens behind 4K to 16K x 8 heads take 230 us (740 TFLOP/s), one prompt of 8192 x 16 heads 595 (925). Short
-// prompts are bound by the start and end of a workgroup, about 6 us (8 of up to 300 tokens x 16 heads: 15 us).
+// What bounds it: the matrix units and the card's power. 8192 tokens x 16 heads (128 + 64 / 128 values, causal) take 353 to
+// 371 us on different cards, 970 to 925 TFLOP/s, where a plain matrix product of the library reaches 1200; with
+// 32 queries to a wave they take 414 (twice the LDS reads for a product). 256 values allow only 32: one prompt of 8192 x 16
+// heads takes 600 to 607 us (910 TFLOP/s). 64 values: 257 us for 16 heads, 480 to 487 for 32 (800 and 850 TFLOP/s). 4 chunks of
+// 512 tokens behind 4K to 16K x 8 heads x 256 values take 226 to 234 us (740 TFLOP/s): their tiles' keys are cut into 1, 2, 2
+// and 3 parts, and the longest part has 6208 keys where an even share is 5216, which alone is 217 us. Short prompts wait for one
+// workgroup's chain: the search of its item and its first tiles, about 6 us, and its steps one after another (8 of up to 300
+// tokens x 16 heads: 15 us, 7 of them for 300 keys).
 #include "hs_latent.h"
 #include "hs_mfma.h"
 
@@ -611,6 +614,10 @@ hipError_t set_lds() {
 // 16 heads with 128 values take 374 and 416 us. But 128 fill the card sooner and hide each other's starts: 8 prompts of up
 // to 300 tokens x 16 heads take 25 and 16 us, 64 of them 93 and 56. With 64 values they are even (32 heads 507 and 482
 // us, 16 heads 258 and 265), and there is one kernel; with 256, the results of 256 queries do not fit into the registers.
+// The estimate takes n_q / R queries and n_k / R keys for each of the R sequences. Where most of a context's requests have no
+// prompt that is far off: 512 queries behind 15872 keys x 16 heads of 128 take 110 us in a context of 1 or 8 requests and 395 in
+// one of 64 or 256 (no parts), and R - 1 workgroups a head begin for nothing (one prompt of 8192 x 16 heads: 352 us in a
+// context of one, 356 of 256, 1.5 ms of 4096).
 PromptPlan prompt_plan(int R, int n_q, int n_k, int heads, int value) {
   PromptPlan best{1, 1, 0};
   if (n_q <= 0) return best;
