@@ -319,3 +319,55 @@ def test_prompt_bad_boundaries_write_only_their_tensors(fault, nope, rope, value
             _within(o.t[a:b, h], w[0], w[2], f"{fault} head {h} o")
             _within(lse.t[a:b, h], w[1], w[3], f"{fault} head {h} lse")
     sw.close()
+
+
+# ---- large values
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("R,k,heads", [(1, 2048, 16), (200, 700, 60), (64, 1500, 128)])
+def test_attend_large_values(R, k, heads, mx):
+    """Latent values of 2^80 behind scores that rise by less than what moves the maximum (weights up to 2^16)."""
+    c = Attend(R, k, k, 0, heads, 512, 64, mx, seed=61)
+    gen = torch.Generator().manual_seed(62)
+    c.out = torch.arange(k, dtype=torch.int32).repeat(R, 1)
+    c.dev["out"] = c.out.cuda()
+    v = torch.zeros(k, 576)
+    v[:, :512] = torch.where(torch.rand(k, 512, generator=gen) < 0.5, -1.0, 1.0) * 2.0 ** 80
+    v[:, 512] = (torch.arange(k) * 10.0 / k).bfloat16().float()
+    if mx:
+        s, at, _ = ref.row_layout(512, 64, True)
+        row = torch.cat([(v[:, :512] * 2.0 ** -80).to(torch.float8_e4m3fn).view(torch.uint8),
+                         torch.full((k, at - s), 207, dtype=torch.uint8), v[:, 512:].bfloat16().view(torch.uint8)], -1)
+    else:
+        row = v.bfloat16().view(torch.uint8)
+    c.rows = row.repeat(R, 1, 1)
+    c.sw.hot.copy_(c.rows)
+    c.q.zero_()
+    c.q[..., 512] = 1.0
+    c.dev["q"] = c.q.cuda()
+    c.scale = 1.0
+    c.run().check({0, R - 1}).close()
+
+
+@pytest.mark.parametrize("nope,value", [(64, 64), (128, 128), (192, 256)])
+@pytest.mark.parametrize("nq,nk,heads", [([300], [300], 4), ([3], [5000], 4), ([200], [200], 512)])
+def test_prompt_large_values(nq, nk, heads, nope, value):
+    gen = torch.Generator().manual_seed(63)
+    sw = hm.SwapIn(hm.config(1, 1, 1, 0.0, 16, 4, 0))
+    N, M = nq[0], nk[0]
+    q = torch.zeros(N, heads, nope + 32).bfloat16()
+    q[..., nope] = 1.0
+    kr = torch.zeros(M, 32)
+    kr[:, 0] = torch.arange(M) * 10.0 / M
+    kr = kr.bfloat16()
+    kv = torch.zeros(M, heads, nope + value)
+    kv[..., nope:] = torch.where(torch.rand(M, heads, value, generator=gen) < 0.5, -1.0, 1.0) * 2.0 ** 80
+    kv = kv.bfloat16()
+    o = torch.full((N, heads, value), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N, heads), 9.0, device="cuda")
+    hm.hs_attend_prompt(sw.ctx, q.cuda(), kv.cuda(), kr.cuda(), _cu(nq).cuda(), _cu(nk).cuda(), 1.0, o, lse)
+    for h in {0, heads - 1}:
+        w = ref.prompt(q[:, h].double(), kv[:, h].double(), kr.double(), nope, 1.0, True)
+        _within(o[:, h], w[0], w[2], f"head {h} o")
+        _within(lse[:, h], w[1], w[3], f"head {h} lse")
+    sw.close()
