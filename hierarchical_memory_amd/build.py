@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhisparse.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("hs_api.cpp", "hs_kernels.hip", "hs_tokens.hip", "hs_attend.hip",
-                                           "hs_prompt.hip")]
+                                           "hs_prompt.hip", "hs_heads.hip", "hs_score.hip",
+                                           "hs_select.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,5 +1,6 @@
 // C ABI of the HiSparse swap-in path: argument checks, the pinned host pool, launches.
 #include "hisparse.h"
+#include "hs_index.h"
 #include "hs_internal.h"
 #include "hs_latent.h"
 
@@ -913,6 +914,244 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
   a.lse = d_lse;
   hipError_t e = hs::launch_prompt(a, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "prompt launch");
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int32_t kMaxIndexHeads = 64;
+
+// A head's format, and the arguments that go with it.
+int check_head(const hs_head_format* f, const void* d_weight, const void* d_bias, const double* d_freqs, hs::HeadArgs* a) {
+  if (!f) return fail(HS_E_INVALID, "head format is NULL");
+  if (f->dim < 32 || f->dim > 256 || f->dim % 32 != 0)
+    return fail(HS_E_INVALID, "a head's dim must be a multiple of 32 in [32, 256] (got %d)", f->dim);
+  if (f->rope < 0 || f->rope > f->dim || f->rope % 16 != 0)
+    return fail(HS_E_INVALID, "a head's rope must be a multiple of 16 in [0, dim] (got %d)", f->rope);
+  if (f->rope_at < 0 || f->rope_at % 8 != 0 || f->rope_at > f->dim - f->rope)
+    return fail(HS_E_INVALID, "a head's rope_at must be a multiple of 8 in [0, dim - rope] (got %d)", f->rope_at);
+  if (f->rope_style != HS_ROPE_PAIRS && f->rope_style != HS_ROPE_HALVES)
+    return fail(HS_E_INVALID, "rope_style must be HS_ROPE_PAIRS (0) or HS_ROPE_HALVES (1) (got %d)", f->rope_style);
+  if (f->norm != HS_NORM_NONE && f->norm != HS_NORM_RMS && f->norm != HS_NORM_LAYER)
+    return fail(HS_E_INVALID, "norm must be HS_NORM_NONE (0), HS_NORM_RMS (1) or HS_NORM_LAYER (2) (got %d)", f->norm);
+  if (!(f->eps >= 0.0f) || !std::isfinite(f->eps))
+    return fail(HS_E_INVALID, "eps must be finite and >= 0 (got %g)", (double)f->eps);
+  if (d_weight && f->norm == HS_NORM_NONE) return fail(HS_E_INVALID, "weight given but the format has no norm");
+  if (d_bias && f->norm != HS_NORM_LAYER) return fail(HS_E_INVALID, "bias given but the format's norm has none");
+  if (!aligned(d_weight, 16) || !aligned(d_bias, 16)) return fail(HS_E_INVALID, "weight and bias must be 16-byte aligned");
+  if (!aligned(d_freqs, 8)) return fail(HS_E_INVALID, "freqs must be 8-byte aligned");
+  a->dim = f->dim;
+  a->rope = f->rope;
+  a->rope_at = f->rope_at;
+  a->halves = f->rope_style == HS_ROPE_HALVES;
+  a->norm = f->norm;
+  a->eps = f->eps;
+  a->weight = (const uint16_t*)d_weight;
+  a->bias = (const uint16_t*)d_bias;
+  a->freqs = f->rope > 0 ? d_freqs : nullptr;
+  return HS_OK;
+}
+
+int check_key(const hs_key_format* key) {
+  if (!key) return fail(HS_E_INVALID, "key format is NULL");
+  if (key->dim != 64 && key->dim != 128) return fail(HS_E_INVALID, "a key's dim must be 64 or 128 (got %d)", key->dim);
+  if (key->type != HS_KEY_MXFP8 && key->type != HS_KEY_MXFP4)
+    return fail(HS_E_INVALID, "a key's type must be HS_KEY_MXFP8 (0) or HS_KEY_MXFP4 (1) (got %d)", key->type);
+  return HS_OK;
+}
+
+uint64_t key_bytes(int R, int H, const hs_key_format* key) {
+  return hs::key_scales_at(R, H, key->dim, key->type) + (uint64_t)R * H * (uint64_t)(key->dim / hs::kMxBlock);
+}
+
+// The key cache of a call.
+int check_keys(const hs_ctx* ctx, const hs_key_format* key, const void* d_keys, uint64_t keys_bytes) {
+  const int rc = check_key(key);
+  if (rc) return rc;
+  if (!d_keys) return fail(HS_E_INVALID, "keys must not be NULL");
+  if (!aligned(d_keys, 16)) return fail(HS_E_INVALID, "keys must be 16-byte aligned");
+  const uint64_t need = key_bytes(ctx->cfg.num_requests, ctx->H, key);
+  if (keys_bytes < need)
+    return fail(HS_E_INVALID, "the key cache has %llu bytes, needs %llu", (unsigned long long)keys_bytes,
+                (unsigned long long)need);
+  return HS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hs_norm_rotate(hs_ctx* ctx, const hs_head_format* fmt, const void* d_x, int64_t x_stride, int64_t x_head_stride,
+                   int32_t heads, const void* d_weight, const void* d_bias, const double* d_freqs, const int32_t* d_pos,
+                   int32_t n_tokens, void* d_o, int64_t o_stride, int64_t o_head_stride, void* d_o_scales, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  hs::HeadArgs a{};
+  rc = check_head(fmt, d_weight, d_bias, d_freqs, &a);
+  if (rc) return rc;
+  rc = check_heads(heads);
+  if (rc) return rc;
+  rc = check_tokens("n_tokens", n_tokens);
+  if (rc) return rc;
+  if (n_tokens > 0 && (!d_x || !d_o)) return fail(HS_E_INVALID, "x and o must not be NULL");
+  if (n_tokens > 0 && a.freqs && !d_pos) return fail(HS_E_INVALID, "pos must not be NULL: the call rotates");
+  if (x_stride < 0 || x_stride % 8 != 0 || x_head_stride < 0 || x_head_stride % 8 != 0)
+    return fail(HS_E_INVALID, "x's strides must be multiples of 8 and >= 0 (got %lld and %lld)", (long long)x_stride,
+                (long long)x_head_stride);
+  if (d_o_scales) {
+    if (o_stride != (int64_t)heads * fmt->dim || o_head_stride != fmt->dim)
+      return fail(HS_E_INVALID, "8-bit outputs are packed: o's strides must be %lld and %d (got %lld and %lld)",
+                  (long long)heads * fmt->dim, fmt->dim, (long long)o_stride, (long long)o_head_stride);
+  } else if (o_stride < fmt->dim || o_stride % 8 != 0 || o_head_stride < fmt->dim || o_head_stride % 8 != 0) {
+    return fail(HS_E_INVALID, "o's strides must be multiples of 8 and at least %d (got %lld and %lld)", fmt->dim,
+                (long long)o_stride, (long long)o_head_stride);
+  }
+  if (!aligned(d_x, 16) || !aligned(d_o, 16)) return fail(HS_E_INVALID, "x and o must be 16-byte aligned");
+  a.heads = heads;
+  a.n = n_tokens;
+  a.x_stride = x_stride;
+  a.x_head_stride = x_head_stride;
+  a.x = (const uint16_t*)d_x;
+  a.pos = d_pos;
+  a.o = (char*)d_o;
+  a.o_stride = o_stride;
+  a.o_head_stride = o_head_stride;
+  a.scales = (uint8_t*)d_o_scales;
+  hipError_t e = hs::launch_heads(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "norm-rotate launch");
+  return ok();
+}
+
+int hs_key_bytes(const hs_config* cfg, const hs_key_format* key, uint64_t* bytes) {
+  if (!bytes) return fail(HS_E_INVALID, "bytes output is NULL");
+  int32_t H;
+  hs::Layout L;
+  int rc = check_config(cfg, &H, &L);
+  if (rc) return rc;
+  rc = check_key(key);
+  if (rc) return rc;
+  *bytes = key_bytes(cfg->num_requests, H, key);
+  return ok();
+}
+
+int hs_store_keys(hs_ctx* ctx, const hs_head_format* fmt, const hs_key_format* key, const void* d_x, int64_t x_stride,
+                  const void* d_weight, const void* d_bias, const double* d_freqs, const int32_t* d_req, const int32_t* d_pos,
+                  int32_t n_tokens, void* d_keys, uint64_t keys_bytes, void* d_values, int32_t* d_status, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  hs::HeadArgs a{};
+  rc = check_head(fmt, d_weight, d_bias, d_freqs, &a);
+  if (rc) return rc;
+  rc = check_keys(ctx, key, d_keys, keys_bytes);
+  if (rc) return rc;
+  if (fmt->dim != key->dim) return fail(HS_E_INVALID, "the head's dim is %d, the key's %d", fmt->dim, key->dim);
+  rc = check_tokens("n_tokens", n_tokens);
+  if (rc) return rc;
+  if (n_tokens > 0 && (!d_x || !d_req || !d_pos)) return fail(HS_E_INVALID, "x, req and pos must not be NULL");
+  if (x_stride % 8 != 0 || x_stride < fmt->dim)
+    return fail(HS_E_INVALID, "x_stride must be a multiple of 8 and at least %d (got %lld)", fmt->dim, (long long)x_stride);
+  if (!aligned(d_x, 16) || !aligned(d_values, 16)) return fail(HS_E_INVALID, "x and values must be 16-byte aligned");
+  a.heads = 1;
+  a.n = n_tokens;
+  a.x_stride = x_stride;
+  a.x = (const uint16_t*)d_x;
+  a.pos = d_pos;
+  a.type = key->type;
+  a.R = ctx->cfg.num_requests;
+  a.H = ctx->H;
+  a.req = d_req;
+  a.keys = (char*)d_keys;
+  a.key_scales = (uint8_t*)d_keys + hs::key_scales_at(a.R, a.H, key->dim, key->type);
+  a.values = (uint16_t*)d_values;
+  a.status = d_status;
+  hipError_t e = hs::launch_store_keys(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "key store launch");
+  return ok();
+}
+
+int hs_score_keys(hs_ctx* ctx, const hs_key_format* key, const void* d_keys, uint64_t keys_bytes, const void* d_q,
+                  const void* d_q_scales, int32_t heads, const float* d_weights, const int32_t* d_req, const int32_t* d_pos,
+                  int32_t n_tokens, float* d_scores, int64_t score_stride, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  rc = check_keys(ctx, key, d_keys, keys_bytes);
+  if (rc) return rc;
+  if (heads < 1 || heads > kMaxIndexHeads)
+    return fail(HS_E_INVALID, "heads must be in [1, %d] (got %d)", kMaxIndexHeads, heads);
+  rc = check_tokens("n_tokens", n_tokens);
+  if (rc) return rc;
+  if (n_tokens > 0 && (!d_q || !d_q_scales || !d_weights || !d_req || !d_pos || !d_scores))
+    return fail(HS_E_INVALID, "q, q_scales, weights, req, pos and scores must not be NULL");
+  if (score_stride < ctx->H)
+    return fail(HS_E_INVALID, "score_stride must be at least %d, a request's positions (got %lld)", ctx->H,
+                (long long)score_stride);
+  if (!aligned(d_q, 16)) return fail(HS_E_INVALID, "q must be 16-byte aligned");
+  hs::ScoreArgs a{};
+  a.dim = key->dim;
+  a.type = key->type;
+  a.heads = heads;
+  a.R = ctx->cfg.num_requests;
+  a.H = ctx->H;
+  a.n = n_tokens;
+  a.keys = (const char*)d_keys;
+  a.key_scales = (const uint8_t*)d_keys + hs::key_scales_at(a.R, a.H, key->dim, key->type);
+  a.q = (const uint8_t*)d_q;
+  a.q_scales = (const uint8_t*)d_q_scales;
+  a.weights = d_weights;
+  a.req = d_req;
+  a.pos = d_pos;
+  a.scores = d_scores;
+  a.stride = score_stride;
+  hipError_t e = hs::launch_score(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "score launch");
+  return ok();
+}
+
+int hs_select_work_bytes(const hs_config* cfg, int32_t rows, int64_t columns, uint64_t* bytes) {
+  if (!bytes) return fail(HS_E_INVALID, "bytes output is NULL");
+  int32_t H;
+  hs::Layout L;
+  int rc = check_config(cfg, &H, &L);
+  if (rc) return rc;
+  rc = check_tokens("rows", rows);
+  if (rc) return rc;
+  if (columns < 0 || columns > (1ll << 31)) return fail(HS_E_INVALID, "columns must be in [0, 2^31] (got %lld)", (long long)columns);
+  *bytes = hs::select_work_bytes(rows, columns, cfg->top_k);
+  return ok();
+}
+
+int hs_select(hs_ctx* ctx, const float* d_scores, int64_t score_stride, const int32_t* d_pos, const int32_t* d_cu,
+              int32_t n_tokens, int32_t recent, int32_t* d_topk, void* d_work, uint64_t work_bytes, void* stream) {
+  int rc = check_ready(ctx);
+  if (rc) return rc;
+  rc = check_tokens("n_tokens", n_tokens);
+  if (rc) return rc;
+  hs::SelectArgs a{};
+  a.rows = d_cu ? ctx->cfg.num_requests : n_tokens;
+  a.n = n_tokens;
+  a.k = ctx->cfg.top_k;
+  if (recent < 0 || recent > a.k) return fail(HS_E_INVALID, "recent must be in [0, %d] (got %d)", a.k, recent);
+  if (n_tokens > 0 && ((score_stride > 0 && !d_scores) || !d_pos))
+    return fail(HS_E_INVALID, "scores and pos must not be NULL");
+  if (a.rows > 0 && !d_topk) return fail(HS_E_INVALID, "topk must not be NULL");
+  if (score_stride < 0 || score_stride % 4 != 0 || score_stride > (1ll << 31))
+    return fail(HS_E_INVALID, "score_stride must be a multiple of 4 in [0, 2^31] (got %lld)", (long long)score_stride);
+  if (!aligned(d_scores, 16) || !aligned(d_work, 16)) return fail(HS_E_INVALID, "scores and work must be 16-byte aligned");
+  const uint64_t need = hs::select_work_bytes(a.rows, score_stride, a.k);
+  if (need > 0 && (!d_work || work_bytes < need))
+    return fail(HS_E_INVALID, "work buffer has %llu bytes, needs %llu", (unsigned long long)(d_work ? work_bytes : 0),
+                (unsigned long long)need);
+  a.recent = recent;
+  a.columns = score_stride;
+  a.scores = d_scores;
+  a.pos = d_pos;
+  a.cu = d_cu;
+  a.topk = d_topk;
+  a.work = (char*)d_work;
+  hipError_t e = hs::launch_select(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "select launch");
   return ok();
 }
 

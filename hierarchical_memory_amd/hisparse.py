@@ -23,12 +23,15 @@ HS_PLAN_ROW_SOURCES = 1
 HS_STATE_TABLES, HS_STATE_ROWS = 1, 2
 HS_ROW_BF16, HS_ROW_MXFP8 = 0, 1
 HS_ROPE_PAIRS, HS_ROPE_HALVES = 0, 1
+HS_NORM_NONE, HS_NORM_RMS, HS_NORM_LAYER = 0, 1, 2
+HS_KEY_MXFP8, HS_KEY_MXFP4 = 0, 1
 
 EXPORTED = ("hs_required_sizes", "hs_create", "hs_host_pool", "hs_bind_device", "hs_reset", "hs_resolve",
             "hs_plan", "hs_copy", "hs_trial", "hs_commit", "hs_offload", "hs_advance_tail", "hs_gather",
             "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state", "hs_row_bytes", "hs_map_tokens",
             "hs_store_rows", "hs_attend_work_bytes", "hs_attend", "hs_attend_prompt_work_bytes",
-            "hs_attend_prompt", "hs_destroy", "hs_last_error")
+            "hs_attend_prompt", "hs_norm_rotate", "hs_key_bytes", "hs_store_keys", "hs_score_keys",
+            "hs_select_work_bytes", "hs_select", "hs_destroy", "hs_last_error")
 HS_STATIC_PLAN_BYTES = 8 << 20
 
 
@@ -63,6 +66,15 @@ class HsSizes(ctypes.Structure):
 
 class HsRowFormat(ctypes.Structure):
     _fields_ = [("latent", ctypes.c_int32), ("rope", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class HsHeadFormat(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("rope", ctypes.c_int32), ("rope_at", ctypes.c_int32),
+                ("rope_style", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class HsKeyFormat(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -107,6 +119,13 @@ def lib():
         L.hs_attend_prompt.argtypes = [vp, vp, vp, vp, i64, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp,
                                        ctypes.c_uint64, vp]
         L.hs_attend_prompt_work_bytes.argtypes = [i32] * 7 + [ctypes.POINTER(ctypes.c_uint64)]
+        head, key, u64 = ctypes.POINTER(HsHeadFormat), ctypes.POINTER(HsKeyFormat), ctypes.c_uint64
+        L.hs_norm_rotate.argtypes = [vp, head, vp, i64, i64, i32, vp, vp, vp, vp, i32, vp, i64, i64, vp, vp]
+        L.hs_key_bytes.argtypes = [ctypes.POINTER(HsConfig), key, ctypes.POINTER(u64)]
+        L.hs_store_keys.argtypes = [vp, head, key, vp, i64, vp, vp, vp, vp, vp, i32, vp, u64, vp, vp, vp]
+        L.hs_score_keys.argtypes = [vp, key, vp, u64, vp, vp, i32, vp, vp, vp, i32, vp, i64, vp]
+        L.hs_select_work_bytes.argtypes = [ctypes.POINTER(HsConfig), i32, i64, ctypes.POINTER(u64)]
+        L.hs_select.argtypes = [vp, vp, i64, vp, vp, i32, i32, vp, vp, u64, vp]
         L.hs_destroy.argtypes = [vp]
         L.hs_destroy.restype = None
         L.hs_last_error.argtypes = []
@@ -115,7 +134,8 @@ def lib():
                      "hs_plan", "hs_copy", "hs_trial", "hs_commit", "hs_offload", "hs_advance_tail", "hs_gather",
                      "hs_rebuild_order", "hs_step_static", "hs_export_state", "hs_import_state", "hs_row_bytes",
                      "hs_map_tokens", "hs_store_rows", "hs_attend_work_bytes", "hs_attend",
-                     "hs_attend_prompt_work_bytes", "hs_attend_prompt"):
+                     "hs_attend_prompt_work_bytes", "hs_attend_prompt", "hs_norm_rotate", "hs_key_bytes",
+                     "hs_store_keys", "hs_score_keys", "hs_select_work_bytes", "hs_select"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -158,10 +178,11 @@ def hs_required_sizes(cfg: HsConfig) -> HsSizes:
 class _Limits:
     """What a context's calls need of their tensor arguments, computed once at hs_create: element counts of
     the int32 arrays and byte counts of the row buffers."""
-    __slots__ = ("R", "RK", "plan", "gather", "trial", "row_bytes")
+    __slots__ = ("R", "RK", "H", "k", "plan", "gather", "trial", "row_bytes")
 
     def __init__(self, cfg: HsConfig, s: HsSizes):
         self.R, self.RK = cfg.num_requests, cfg.num_requests * cfg.top_k
+        self.H, self.k = s.host_rows, cfg.top_k
         self.plan, self.gather, self.trial = s.plan_bytes // 4, s.gather_bytes, s.trial_bytes
         self.row_bytes = cfg.row_bytes
 
@@ -593,6 +614,180 @@ def hs_attend_prompt(ctx, q, kv, rope, cu_q, cu_k, scale: float, o, lse=None, ca
                                   o.data_ptr(), _at(lse), _at(work), _bytes(work), _raw_stream(stream, dev)))
 
 
+def head_format(dim: int, rope: int = 0, rope_at: int = 0, rope_style: int = HS_ROPE_PAIRS, norm: int = HS_NORM_NONE,
+                eps: float = 0.0) -> HsHeadFormat:
+    """How a head's vector is made: its values, the part of it that is rotated, its norm (HS_NORM_*)."""
+    return HsHeadFormat(dim, rope, rope_at, rope_style, norm, eps)
+
+
+def key_format(dim: int = 128, key_type: int = HS_KEY_MXFP8) -> HsKeyFormat:
+    """Format of the index keys: values, HS_KEY_MXFP8 or HS_KEY_MXFP4."""
+    return HsKeyFormat(dim, key_type)
+
+
+def hs_key_bytes(cfg: HsConfig, key: HsKeyFormat) -> int:
+    n = ctypes.c_uint64()
+    _check(lib().hs_key_bytes(ctypes.byref(cfg), ctypes.byref(key), ctypes.byref(n)))
+    return n.value
+
+
+def key_parts(cfg: HsConfig, key: HsKeyFormat, keys):
+    """The values [R, H, bytes of a key] and the scales [R, H, dim / 32] of a key cache, as uint8 views."""
+    R, H = cfg.num_requests, hs_required_sizes(cfg).host_rows
+    width, blocks = key.dim // 2 if key.type == HS_KEY_MXFP4 else key.dim, key.dim // 32
+    at = -(-R * H * width // 256) * 256
+    flat = keys.view(-1)
+    return flat[:R * H * width].view(R, H, width), flat[at:at + R * H * blocks].view(R, H, blocks)
+
+
+def _strides(name: str, x, dim: int):
+    """(token, head) strides of x [n, heads, dim], those of a dimension of one element set to what packed ones have."""
+    if x.dim() != 3 or x.shape[2] != dim:
+        raise ValueError(f"{name} must have shape [n, heads, {dim}], got {list(x.shape)}")
+    n, heads, _ = x.shape
+    token, head, one = x.stride()
+    if one != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    head = head if heads > 1 else dim
+    return (token if n > 1 else max(dim, heads * head)), head
+
+
+def hs_norm_rotate(ctx, fmt: HsHeadFormat, x, weight, bias, freqs, pos, o, scales=None, stream=None) -> None:
+    """x: device bf16 [n, heads, dim], tokens and heads of any strides that are multiples of 8; weight, bias: bf16 [dim] or
+    None; freqs: float64 [rope / 2] or None; pos: int32 [n] (None: no rotation, no token skipped); o: bf16 [n, heads, dim],
+    strided like x (x itself for a call in place), or, with scales (uint8 [n, heads, dim / 32]), float8_e4m3fn."""
+    t = _t()
+    bf16 = t.bfloat16
+    D = fmt.dim
+    for name, v in (("x", x), ("o", o)):
+        if v is None:
+            raise ValueError(f"{name} must not be None")
+    if x.dtype is not bf16:
+        raise ValueError(f"x must be a {bf16} tensor, got {x.dtype}")
+    (xt, xh), (ot, oh) = _strides("x", x, D), _strides("o", o, D)
+    n, heads, _ = x.shape
+    if o.shape != x.shape:
+        raise ValueError(f"o must have shape {list(x.shape)}, got {list(o.shape)}")
+    dev = x.get_device()
+    kind = bf16 if scales is None else t.float8_e4m3fn
+    if not (o.dtype is kind and o.get_device() == dev and (scales is None or o.is_contiguous())
+            and (weight is None or _fine(weight, bf16, (D,), dev)) and (bias is None or _fine(bias, bf16, (D,), dev))
+            and (freqs is None or _fine(freqs, t.float64, (fmt.rope // 2,), dev))
+            and (pos is None or _fine(pos, t.int32, (n,), dev))
+            and (scales is None or _fine(scales, t.uint8, (n, heads, D // 32), dev))
+            and dev >= 0 and dev == t._C._cuda_getDevice()):
+        _refuse(_current(dev), ("x", x[:0], None, None, False), ("weight", weight, bf16, (D,), True),
+                ("bias", bias, bf16, (D,), True), ("freqs", freqs, t.float64, (fmt.rope // 2,), True),
+                ("pos", pos, t.int32, (n,), True), ("o", o[:0] if scales is None else o, kind, None, False),
+                ("scales", scales, t.uint8, (n, heads, D // 32), True))
+    _check(lib().hs_norm_rotate(ctx, ctypes.byref(fmt), x.data_ptr(), xt, xh, heads, _at(weight), _at(bias), _at(freqs),
+                                _at(pos), n, o.data_ptr(), ot, oh, _at(scales), _raw_stream(stream, dev)))
+
+
+def hs_store_keys(ctx, fmt: HsHeadFormat, key: HsKeyFormat, x, weight, bias, freqs, req, pos, keys, values=None, status=None,
+                  stream=None) -> None:
+    """x: device bf16 [n, dim], rows of any stride that is a multiple of 8; weight, bias: bf16 [dim] or None; freqs: float64
+    [rope / 2] or None; req, pos: int32 [n] as hs_map_tokens wrote them; keys: the key cache (hs_key_bytes); values: bf16
+    [n, dim] output or None."""
+    t = _t()
+    bf16, i32 = t.bfloat16, t.int32
+    lim = _CTX_SIZES.get(_ctx_key(ctx))
+    R = lim.R if lim is not None else 0
+    D = fmt.dim
+    if x is None:
+        raise ValueError("x must not be None")
+    if x.dtype is not bf16:
+        raise ValueError(f"x must be a {bf16} tensor, got {x.dtype}")
+    if x.dim() != 2 or x.shape[1] != D:
+        raise ValueError(f"x must have shape [n, {D}], got {list(x.shape)}")
+    n, (step, one) = x.shape[0], x.stride()
+    if one != 1:
+        raise ValueError("x must have contiguous rows")
+    dev = x.get_device()
+    if not ((weight is None or _fine(weight, bf16, (D,), dev)) and (bias is None or _fine(bias, bf16, (D,), dev))
+            and (freqs is None or _fine(freqs, t.float64, (fmt.rope // 2,), dev)) and _fine(req, i32, (n,), dev)
+            and _fine(pos, i32, (n,), dev) and keys is not None and keys.get_device() == dev and keys.is_contiguous()
+            and (values is None or _fine(values, bf16, (n, D), dev)) and (status is None or _i32_fine(status, R, dev))
+            and dev >= 0 and dev == t._C._cuda_getDevice()):
+        _refuse(_current(dev), ("weight", weight, bf16, (D,), True), ("bias", bias, bf16, (D,), True),
+                ("freqs", freqs, t.float64, (fmt.rope // 2,), True), ("req", req, i32, (n,), False),
+                ("pos", pos, i32, (n,), False), ("keys", keys, None, None, False), ("values", values, bf16, (n, D), True),
+                ("status", status, i32, R, True), ("x", x[:0], None, None, False))
+    _check(lib().hs_store_keys(ctx, ctypes.byref(fmt), ctypes.byref(key), x.data_ptr(), step if n > 1 else D, _at(weight),
+                               _at(bias), _at(freqs), req.data_ptr(), pos.data_ptr(), n, keys.data_ptr(), _bytes(keys),
+                               _at(values), _at(status), _raw_stream(stream, dev)))
+
+
+def hs_score_keys(ctx, key: HsKeyFormat, keys, q, q_scales, weights, req, pos, scores, stream=None) -> None:
+    """keys: the key cache; q: float8_e4m3fn [n, heads, dim] with q_scales uint8 [n, heads, dim / 32], as hs_norm_rotate wrote
+    them; weights: float32 [n, heads]; req, pos: int32 [n]; scores: float32 [n, at least the context's positions], rows of
+    any stride."""
+    t = _t()
+    f8, f32, i32, u8 = t.float8_e4m3fn, t.float32, t.int32, t.uint8
+    lim = _CTX_SIZES.get(_ctx_key(ctx))
+    D = key.dim
+    if q is None or scores is None:
+        raise ValueError(f"{'q' if q is None else 'scores'} must not be None")
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must have shape [n, heads, {D}], got {list(q.shape)}")
+    n, heads, _ = q.shape
+    if scores.dim() != 2 or scores.shape[0] != n or (lim is not None and scores.shape[1] < lim.H):
+        raise ValueError(f"scores must have shape [{n}, at least {lim.H if lim is not None else 'H'}], got "
+                         f"{list(scores.shape)}")
+    step, one = scores.stride()
+    if one != 1 and scores.shape[1] > 1 or n > 1 and step < scores.shape[1]:
+        raise ValueError("scores must have contiguous rows")
+    dev = q.get_device()
+    if not (q.dtype is f8 and q.is_contiguous() and _fine(q_scales, u8, (n, heads, D // 32), dev)
+            and _fine(weights, f32, (n, heads), dev) and _fine(req, i32, (n,), dev) and _fine(pos, i32, (n,), dev)
+            and keys is not None and keys.get_device() == dev and keys.is_contiguous() and scores.dtype is f32
+            and scores.get_device() == dev and dev >= 0 and dev == t._C._cuda_getDevice()):
+        _refuse(_current(dev), ("q", q, f8, None, False), ("q_scales", q_scales, u8, (n, heads, D // 32), False),
+                ("weights", weights, f32, (n, heads), False), ("req", req, i32, (n,), False),
+                ("pos", pos, i32, (n,), False), ("keys", keys, None, None, False),
+                ("scores", scores[:0], f32, None, False))
+    _check(lib().hs_score_keys(ctx, ctypes.byref(key), keys.data_ptr(), _bytes(keys), q.data_ptr(), q_scales.data_ptr(),
+                               heads, weights.data_ptr(), req.data_ptr(), pos.data_ptr(), n, scores.data_ptr(),
+                               step if n > 1 else scores.shape[1], _raw_stream(stream, dev)))
+
+
+def hs_select_work_bytes(cfg: HsConfig, rows: int, columns: int) -> int:
+    n = ctypes.c_uint64()
+    _check(lib().hs_select_work_bytes(ctypes.byref(cfg), rows, columns, ctypes.byref(n)))
+    return n.value
+
+
+def hs_select(ctx, scores, pos, topk, cu=None, recent: int = 0, work=None, stream=None) -> None:
+    """scores: device float32 [n, columns] as hs_score_keys wrote them, rows of one stride; pos: int32 [n]; topk: int32
+    [n, k], or with cu (int32 [R + 1]) [R, k]; work: a device buffer of hs_select_work_bytes (rows, the scores' row
+    stride)."""
+    t = _t()
+    f32, i32 = t.float32, t.int32
+    lim = _CTX_SIZES.get(_ctx_key(ctx))
+    R, k = (lim.R, lim.k) if lim is not None else (0, 0)
+    if scores is None:
+        raise ValueError("scores must not be None")
+    if scores.dim() != 2:
+        raise ValueError(f"scores must have shape [n, columns], got {list(scores.shape)}")
+    n, columns = scores.shape
+    step, one = scores.stride()
+    if one != 1 and columns > 1:
+        raise ValueError("scores must have contiguous rows")
+    step = step if n > 1 else columns
+    if columns > 0 and step != columns:
+        raise ValueError(f"scores' rows must lie {columns} elements apart, got {step}")
+    rows = n if cu is None else R
+    dev = scores.get_device()
+    if not (scores.dtype is f32 and _i32_fine(pos, n, dev) and (cu is None or _i32_fine(cu, R + 1, dev))
+            and _i32_fine(topk, rows * k, dev)
+            and (work is None or (work.get_device() == dev and work.is_contiguous()))
+            and dev >= 0 and dev == t._C._cuda_getDevice()):
+        _refuse(_current(dev), ("scores", scores[:0], f32, None, False), ("pos", pos, i32, n, False),
+                ("cu", cu, i32, R + 1, True), ("topk", topk, i32, rows * k, False), ("work", work, None, None, True))
+    _check(lib().hs_select(ctx, scores.data_ptr(), columns, pos.data_ptr(), _at(cu), n, recent, topk.data_ptr(), _at(work),
+                           _bytes(work), _raw_stream(stream, dev)))
+
+
 def hs_rebuild_order(ctx, stream=None) -> None:
     _check(lib().hs_rebuild_order(ctx, _stream(stream)))
 
@@ -679,6 +874,17 @@ class SwapIn:
         """A work buffer for hs_attend (None where it takes none)."""
         import torch
         n = hs_attend_work_bytes(self.cfg, fmt, heads)
+        return torch.empty((n,), dtype=torch.uint8, device=self.device) if n else None
+
+    def key_cache(self, key: HsKeyFormat):
+        """A key cache for hs_store_keys and hs_score_keys, zeroed."""
+        import torch
+        return torch.zeros((hs_key_bytes(self.cfg, key),), dtype=torch.uint8, device=self.device)
+
+    def select_work(self, rows: int, columns: int):
+        """A work buffer for hs_select (None where it takes none)."""
+        import torch
+        n = hs_select_work_bytes(self.cfg, rows, columns)
         return torch.empty((n,), dtype=torch.uint8, device=self.device) if n else None
 
     def close(self) -> None:

@@ -443,6 +443,117 @@ int hs_attend_prompt(hs_ctx* ctx, const void* d_q, const void* d_kv, const void*
                      int32_t rope, int32_t value, float scale, int32_t causal, void* d_o, float* d_lse, void* d_work,
                      uint64_t work_bytes, void* stream);
 
+/*
+ * The selection itself: what a decode step computes before hs_resolve. Every token leaves an index key in a cache on the
+ * device; a new token's index queries are scored against the keys of its whole context, and the best positions are the
+ * ids that hs_resolve takes. The calls read hs_map_tokens' outputs and write hs_resolve's input:
+ *   hs_norm_rotate (the queries), hs_store_keys, hs_score_keys, hs_select
+ *
+ * A head's vector, as the first two compute it from a projection's output v (bf16, dim values):
+ *   HS_NORM_NONE   y = v
+ *   HS_NORM_RMS    y = v / sqrt(mean of v^2 + eps) * weight
+ *   HS_NORM_LAYER  y = (v - mean) / sqrt(mean of (v - mean)^2 + eps) * weight + bias
+ * and the pairs of y[rope_at .. rope_at + rope) turned by the token's position times the pair's frequency, in 32 bits (angles
+ * and what they lose of their whole turns in 64), without a rounding in between. It is rounded once, to bf16 or to microscaled
+ * values: blocks of 32 under one scale byte b (e8m0, 2^(b - 127)), the least power of two, 2^-100 at least, that keeps the
+ * block within the type's largest value (e4m3: 448, e2m1: 6). A block that holds an infinity or a NaN gets the scale byte
+ * 255, and every value of it is a NaN.
+ */
+#define HS_NORM_NONE 0
+#define HS_NORM_RMS 1
+#define HS_NORM_LAYER 2
+typedef struct hs_head_format {
+  int32_t dim;        /* values of a head: a multiple of 32, 32 .. 256 */
+  int32_t rope;       /* values of the rotated part: a multiple of 16, 0 .. dim */
+  int32_t rope_at;    /* where it begins: a multiple of 8, rope_at + rope <= dim */
+  int32_t rope_style; /* HS_ROPE_PAIRS or HS_ROPE_HALVES, within the rotated part */
+  int32_t norm;       /* HS_NORM_* */
+  float eps;          /* of the norm, finite and >= 0 */
+} hs_head_format;
+
+/*
+ * The heads of n_tokens tokens: normed, rotated and rounded in one pass (index queries in 8 bits, attention queries in bf16).
+ *   d_x        value i of head h of token t at d_x + t * x_stride + h * x_head_stride + i (bf16 elements; 16-byte aligned,
+ *              strides multiples of 8 and >= 0)
+ *   d_weight, d_bias  bf16 [dim], 16-byte aligned, or NULL (one, zero); only where the norm has them
+ *   d_freqs    [rope / 2] double, radians per position, 8-byte aligned, or NULL (no rotation)
+ *   d_pos      [n_tokens] positions; tokens with one below 0 are skipped (their outputs are left as they were). NULL: none is
+ *              skipped, which needs a call without rotation
+ *   d_o        d_o_scales NULL: bf16, addressed as d_x is by o_stride and o_head_stride (multiples of 8, >= dim; no two heads
+ *              may overlap). It may be d_x with the same strides; any other overlap is not allowed
+ *              else: e4m3 [n_tokens][heads][dim] (o_stride heads * dim, o_head_stride dim). 16-byte aligned
+ *   d_o_scales e8m0 [n_tokens][heads][dim / 32], or NULL
+ * heads: 1 .. 512; n_tokens from 0 to 2^30.
+ */
+int hs_norm_rotate(hs_ctx* ctx, const hs_head_format* fmt, const void* d_x, int64_t x_stride, int64_t x_head_stride,
+                   int32_t heads, const void* d_weight, const void* d_bias, const double* d_freqs, const int32_t* d_pos,
+                   int32_t n_tokens, void* d_o, int64_t o_stride, int64_t o_head_stride, void* d_o_scales, void* stream);
+
+/*
+ * The index-key cache: caller-owned device memory of hs_key_bytes bytes, 16-byte aligned, a key for each of a request's H
+ * positions (all of them on the device: a key is a small part of a row).
+ *   HS_KEY_MXFP8  values e4m3 [R][H][dim]
+ *   HS_KEY_MXFP4  values e2m1 [R][H][dim / 2], the even one of a pair in the low four bits
+ * and behind them, at the next multiple of 256 bytes, the scales, e8m0 [R][H][dim / 32]. Nothing in it has to start at zero,
+ * and no call but hs_store_keys writes it (a reset request's keys are overwritten as its new tokens come).
+ */
+#define HS_KEY_MXFP8 0
+#define HS_KEY_MXFP4 1
+typedef struct hs_key_format {
+  int32_t dim;  /* 64 or 128 */
+  int32_t type; /* HS_KEY_MXFP8 or HS_KEY_MXFP4 */
+} hs_key_format;
+
+/* Bytes of the key cache of a configuration. Host-only. */
+int hs_key_bytes(const hs_config* cfg, const hs_key_format* key, uint64_t* bytes);
+
+/*
+ * New tokens' index keys, normed, rotated and quantised as they are written to the cache. fmt->dim must be key->dim. Token t's
+ * input is d_x[t * x_stride .. + dim) (bf16, 16-byte aligned, x_stride a multiple of 8, at least dim); d_weight, d_bias and
+ * d_freqs as in hs_norm_rotate. Its key becomes that of request d_req[t], position d_pos[t]. Tokens with either below 0 are
+ * skipped; one with another value out of range is skipped too and, where its request is one, sets HS_STATUS_BAD_ID in
+ * d_status[r] (optional; not written otherwise). Two tokens of one call must not name the same position.
+ * d_values ([n_tokens][dim] bf16, 16-byte aligned, or NULL) receives the keys as the cache holds them (a microscaled value is
+ * exact in bf16 from 2^-126 up, and only smaller ones are rounded); rows of skipped tokens are left as they were.
+ */
+int hs_store_keys(hs_ctx* ctx, const hs_head_format* fmt, const hs_key_format* key, const void* d_x, int64_t x_stride,
+                  const void* d_weight, const void* d_bias, const double* d_freqs, const int32_t* d_req, const int32_t* d_pos,
+                  int32_t n_tokens, void* d_keys, uint64_t keys_bytes, void* d_values, int32_t* d_status, void* stream);
+
+/*
+ * Index scores of tokens against the keys of their contexts: for token t of request r at position p, and x in [0, p],
+ *   s[t][x] = sum over heads h of d_weights[t][h] * max(0, q[t][h] . key[r][x])
+ *   d_q, d_q_scales  the heads' queries as hs_norm_rotate leaves them in 8 bits: e4m3 [n_tokens][heads][dim], 16-byte aligned,
+ *                    and e8m0 [n_tokens][heads][dim / 32]
+ *   d_weights  [n_tokens][heads] float32
+ *   d_req, d_pos  [n_tokens]; tokens with a request outside [0, R) or a position outside [0, H) are skipped
+ *   d_scores   float32, token t's at d_scores + t * score_stride (elements, at least H); what lies behind position p, and the
+ *              rows of skipped tokens, are left as they were
+ * heads: 1 .. 64. Values of queries and keys times their scales are exact in the products as long as they are 0 or at least
+ * 2^-126 in magnitude and below 2^128; products and sums are held in 32 bits, in a fixed order, so equal inputs give equal bits.
+ * A NaN in a query or a key makes the scores that read it NaN, whatever the weights.
+ */
+int hs_score_keys(hs_ctx* ctx, const hs_key_format* key, const void* d_keys, uint64_t keys_bytes, const void* d_q,
+                  const void* d_q_scales, int32_t heads, const float* d_weights, const int32_t* d_req, const int32_t* d_pos,
+                  int32_t n_tokens, float* d_scores, int64_t score_stride, void* stream);
+
+/*
+ * The k = top_k best positions of each token's scores, ids for hs_resolve.
+ *   d_scores, score_stride  as hs_score_keys wrote them, 16-byte aligned, the stride a multiple of 4; token t has the positions
+ *             0 .. min(d_pos[t], score_stride - 1), none where d_pos[t] < 0. What lies behind is not read into any result
+ *   d_cu      NULL: row t of d_topk is token t's, for n_tokens rows. Else [R + 1] (hs_map_tokens'): row r is that of the last of
+ *             request r's tokens, d_cu[r + 1] - 1, for R rows; a request without a token in [0, n_tokens) has none
+ *   recent    the last `recent` positions (0 .. top_k) are selected whatever their scores
+ *   d_topk    [rows][k] int32: the selected positions, ascending, and -1 behind them
+ * Of equal scores (zeros of both signs are equal) the lower positions are taken first. A NaN or -inf is never selected unless it
+ * is recent; fewer than k others leave fewer than k ids. The selection is exact, whatever the scores.
+ *   d_work    hs_select_work_bytes bytes of device memory, 16-byte aligned (NULL where that is 0), as in hs_attend
+ * hs_select_work_bytes: `rows` rows (n_tokens, or R with d_cu) of `columns` (score_stride) positions.
+ */
+int hs_select_work_bytes(const hs_config* cfg, int32_t rows, int64_t columns, uint64_t* bytes);
+int hs_select(hs_ctx* ctx, const float* d_scores, int64_t score_stride, const int32_t* d_pos, const int32_t* d_cu,
+              int32_t n_tokens, int32_t recent, int32_t* d_topk, void* d_work, uint64_t work_bytes, void* stream);
+
 /* Free the host pool and the context (device buffers belong to the caller). NULL is ignored. */
 void hs_destroy(hs_ctx* ctx);
 
