@@ -25,12 +25,12 @@ FLAGS = [
     "-I", INCLUDE, "-I", CSRC,
 ]
 
-# The attention kernels: matrix instructions whose results other instructions read (scores) write to the ordinary registers
+# The attention and score kernels: matrix instructions whose results other instructions read (scores) write to the ordinary registers
 MFMA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 
 
 def flags_of(src: str):
-    return FLAGS + (MFMA_FLAGS if os.path.basename(src) in ("hs_attend.hip", "hs_prompt.hip") else [])
+    return FLAGS + (MFMA_FLAGS if os.path.basename(src) in ("hs_attend.hip", "hs_prompt.hip", "hs_score.hip") else [])
 
 
 def build(verbose: bool = False) -> str:
