@@ -1,11 +1,14 @@
 // The k best positions of each row of scores, ascending (gfx950).
 //
-// A workgroup reads its part of a row once, into registers, 64 consecutive positions to a wave's load, so that what is selected
-// leaves in order by ballots. The k-th best score is found without a sort: scores are counted in 2048 bins between the lowest and
-// the highest of them, even in value (which keeps a wave's counts apart, where the bits of the scores would share few bins); the
-// scores of the one bin that the k-th lies in, some dozens, are ranked against each other with their positions. A bin of more
-// than kList (few different scores, or outliers that stretch the range) is divided further by the scores' bits instead, and the
-// positions of equal ones are counted in order. The selection is then a comparison with one score and one position.
+// A workgroup reads its part of a row once, into registers, 64 consecutive positions to a wave's load. What is selected is kept as
+// a mask of each such load, and a thread then writes the positions of one mask: passes over the registers are unrolled code that
+// runs once and waits for its own instructions, and three of them are enough (with two more, to count and to write by ballots,
+// 256 rows of 40960 took 31 us). The k-th best score is found without a sort. It is no lower than the lowest of the threads' own
+// best (or second best) scores, where that makes k of them; what lies above is counted in 2048 bins, even in value (which keeps a
+// wave's counts apart, where the bits of the scores would share few bins), and the scores of the one bin that the k-th lies in,
+// some dozens, are ranked against each other with their positions. A bin of more than kList (few different scores, or outliers
+// that stretch the range) is divided further, by the scores' bits, until kList are left or all are equal; the first of the
+// equal ones are then taken in order.
 // A row of more than kMost positions is cut into parts, whose best k (with their positions, in order) are the row of the next
 // launch; ties stay with the lowest positions, as every launch keeps the order.
 #include "hs_index.h"
@@ -50,11 +53,20 @@ __device__ __forceinline__ int wave_scan(int v) {  // inclusive
   return v;
 }
 
-// kPer: most scores of a thread.
-template <int kPer>
-__global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectArgs a, SelectLevel l) {
+template <class Op>
+__device__ __forceinline__ float wave_reduce(float v, Op op) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = op(v, __shfl_xor(v, d));
+  return v;
+}
+
+// kPer: most scores of a thread, kBlock of them in a block: a workgroup passes over as many blocks as its part has.
+template <int kPer, int kBlock>
+__global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_kernel(SelectArgs a, SelectLevel l) {
   __shared__ int hist[kBins];
   __shared__ uint64_t list[kList];
+  __shared__ int rank[kList];
+  __shared__ uint64_t masks[kSelectWaves * kPer], ties[kSelectWaves * kPer];  // of the loads, in the order of the positions
   __shared__ int sums[kSelectWaves], found[4];
   __shared__ float lows[kSelectWaves], highs[kSelectWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -62,7 +74,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectArgs a, Se
   const int part = (int)(blockIdx.x % l.parts);
   const bool whole = l.out == nullptr;
   // the positions of the row's token, those that compete, and how many of them are selected
-  int64_t m, rivals, from = row;  // from: row of the scores
+  int64_t m, from = row;  // from: row of the scores
   {
     int64_t t = row;
     if (a.cu) {
@@ -74,190 +86,263 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectArgs a, Se
     if (!l.idx) from = t < 0 ? 0 : t;
   }
   const int recent = m < a.recent ? (int)m : a.recent, k = a.k - recent;
-  rivals = l.idx ? l.n_in : m - recent;
-  const int64_t begin = part * l.part;
+  const int64_t rivals = l.idx ? l.n_in : m - recent, begin = part * l.part;
   const int n = (int)(rivals <= begin ? 0 : rivals - begin < l.part ? rivals - begin : l.part);
-  const float* in = l.in + from * l.n_in + begin;
-
-  const int per = (n + kSelectThreads - 1) / kSelectThreads;  // of a thread
-  const int first = wave * per * 64;                          // of the wave
+  const int blocks = (n + kSelectThreads * kBlock - 1) / (kSelectThreads * kBlock);
+  const int first = wave * blocks * kBlock * 64;  // of the wave
   float x[kPer];
+  // f(j) for the wave's loads, in their order
+  auto each = [&](auto f) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (j < per) {
-      const int i = first + j * 64 + lane;
-      x[j] = i < n ? in[i] : -INFINITY;
-    }
+    for (int b = 0; b < kPer / kBlock; ++b)
+      if (b < blocks) {
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+          asm volatile("" : "+v"(x[b * kBlock + i]));  // nothing that a pass works out is kept for the next: registers are short
+          f(b * kBlock + i);
+        }
+      }
+  };
+  {
+    const float* in = l.in + from * l.n_in + begin + first;
+#pragma unroll
+    for (int b = 0; b < kPer / kBlock; ++b)
+      if (b < blocks) {
+        const int left = n - first - b * kBlock * 64;  // of the part, from this block on
+        if (left >= kBlock * 64) {
+#pragma unroll
+          for (int i = 0; i < kBlock; ++i) x[b * kBlock + i] = in[(b * kBlock + i) * 64 + lane];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kBlock; ++i) x[b * kBlock + i] = i * 64 + lane < left ? in[(b * kBlock + i) * 64 + lane] : -INFINITY;
+        }
+      }
+  }
   hist[tid] = hist[tid + kSelectThreads] = 0;
+  if (tid < kList) rank[tid] = 0;
   if (tid == 0) found[3] = 0;
   // a NaN becomes -infinity: what is never selected has one form, and no comparison below meets a NaN
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (j < per) x[j] = x[j] == x[j] ? x[j] : -INFINITY;
-  float lo = INFINITY, hi = -INFINITY;
-  int valid = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (j < per) {
-      const bool is = x[j] > -INFINITY;
-      lo = fminf(lo, is ? x[j] : INFINITY);
-      hi = fmaxf(hi, is && x[j] < INFINITY ? x[j] : -INFINITY);
-      valid += __popcll(__ballot(is));
-    }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    lo = fminf(lo, __shfl_xor(lo, d));
-    hi = fmaxf(hi, __shfl_xor(hi, d));
-  }
-  if (lane == 0) lows[wave] = lo, highs[wave] = hi, sums[wave] = valid;
+  float best = -INFINITY, second = -INFINITY;
+  each([&](int j) {
+    x[j] = x[j] == x[j] ? x[j] : -INFINITY;
+    second = __builtin_amdgcn_fmed3f(x[j], best, second);
+    best = fmaxf(best, x[j]);
+  });
+  const auto lesser = [](float u, float v) { return fminf(u, v); };
+  const auto larger = [](float u, float v) { return fmaxf(u, v); };
+  float hi = wave_reduce(best, larger);
+  float lo = wave_reduce(k <= kSelectThreads ? best : k <= 2 * kSelectThreads ? second : -INFINITY, lesser);
+  if (lane == 0) lows[wave] = lo, highs[wave] = hi;
   __syncthreads();
-  valid = 0;
 #pragma unroll
   for (int w = 0; w < kSelectWaves; ++w) {
     lo = fminf(lo, lows[w]);
     hi = fmaxf(hi, highs[w]);
-    valid += sums[w];
   }
-  // what is selected: a score above `least`, or equal to it up to the position `last`
-  float least = -INFINITY;
-  int last = -1;
-  if (valid > k) {
-    // (a range that is zero or past 32 bits puts every finite score, or all but the lowest, into one bin)
-    const float step = (float)(kBins - 1) / (hi - lo);
-    auto bin_of = [&](float v) {
-      const float b = (v - lo) * step;
-      return b > 0.0f ? b < (float)(kBins - 1) ? (int)b : kBins - 1 : 0;  // (a NaN: 0)
+  // the loads' masks of f(j), to LDS
+  auto mask_of = [&](uint64_t* to, auto f) {
+    uint32_t low = 0, high = 0;
+    each([&](int j) {
+      const uint64_t mask = __ballot(f(j));
+      low = lane == j ? (uint32_t)mask : low;
+      high = lane == j ? (uint32_t)(mask >> 32) : high;
+    });
+    if (lane < blocks * kBlock) to[wave * blocks * kBlock + lane] = (uint64_t)high << 32 | low;
+  };
+  int tied = 0;        // of the equal scores in `ties`, those that are selected
+  bool every = false;  // what may be selected is
+  if (lo == -INFINITY) {
+    // too few scores for that bound: the lowest that may be selected, and how many may
+    int valid = 0;
+    lo = INFINITY;
+    each([&](int j) {
+      lo = fminf(lo, x[j] > -INFINITY ? x[j] : INFINITY);
+      valid += __popcll(__ballot(x[j] > -INFINITY));
+    });
+    lo = wave_reduce(lo, lesser);
+    __syncthreads();  // the bounds before are read
+    if (lane == 0) lows[wave] = lo, sums[wave] = valid;
+    __syncthreads();
+    valid = 0;
+#pragma unroll
+    for (int w = 0; w < kSelectWaves; ++w) {
+      lo = fminf(lo, lows[w]);
+      valid += sums[w];
+    }
+    every = valid <= k;
+  }
+  // Of the counts, the one that the need-th from the highest on lies in (found[0]), and which of its own that is (found[1]);
+  // returns the sum of all
+  auto find = [&](int need) {
+    const int b = kBins - 2 - 2 * tid, upper = hist[b + 1], both = upper + hist[b], upto = wave_scan(both);
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    int before = upto - both, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSelectWaves; ++w) {
+      if (w < wave) before += sums[w];
+      all += sums[w];
+    }
+    if (before < need && before + both >= need) {  // one thread
+      const bool in_upper = before + upper >= need;
+      found[0] = in_upper ? b + 1 : b;
+      found[1] = in_upper ? need - before : need - before - upper;
+    }
+    __syncthreads();
+    return all;
+  };
+  if (k == 0 || every) {
+    mask_of(masks, [&](int j) { return every && x[j] > -INFINITY; });
+    __syncthreads();
+  } else {
+    // The bin of a score from lo on: even in value, between halves so that no difference is past 32 bits. The k-th best is lo
+    // itself where no k are above it; those that are equal to lo need no count (there may be many: scores of zero).
+    lo = fminf(lo, 3.4028235e38f);
+    hi = fminf(hi, 3.4028235e38f);
+    const float half_lo = 0.5f * lo, step = fminf((float)(kBins - 1) / (0.5f * hi - half_lo), 3.4028235e38f);
+    auto place_of = [&](float v) { return fminf(fmaf(v, 0.5f, -half_lo) * step, (float)(kBins - 1)); };
+    each([&](int j) {
+      if (x[j] > lo) atomicAdd(&hist[(uint32_t)place_of(x[j])], 1);
+    });
+    __syncthreads();
+    const int above = find(k);
+    bool equal = above < k;
+    const int bin = equal ? 0 : found[0];
+    int need = equal ? k - above : found[1], count = equal ? 0 : hist[bin];
+    uint32_t from_order = order_of(lo), span = 0xffffffffu;  // of the scores in question
+    const float bin_from = (float)bin, bin_to = (float)(bin + 1);
+    auto is_in = [&](float v) {
+      const float p = place_of(v);
+      return v > lo && p >= bin_from && p < bin_to && order_of(v) - from_order <= span;
     };
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (j < per && x[j] > -INFINITY) atomicAdd(&hist[bin_of(x[j])], 1);
-    __syncthreads();
-    {
-      const int b = kBins - 2 - 2 * tid, upper = hist[b + 1], both = upper + hist[b];
-      const int upto = wave_scan(both);
-      if (lane == 63) sums[wave] = upto;
-      __syncthreads();
-      int before = upto - both;
-#pragma unroll
-      for (int w = 0; w < kSelectWaves; ++w)
-        if (w < wave) before += sums[w];
-      if (before < k && before + both >= k) {  // (one thread; none where k is zero)
-        const bool in_upper = before + upper >= k;
-        found[0] = in_upper ? b + 1 : b;
-        found[1] = in_upper ? k - before : k - before - upper;
-      }
-      if (k == 0 && tid == 0) found[0] = kBins, found[1] = 0;
+    auto add_to_list = [&](int j) {
+      list[atomicAdd(&found[3], 1)] = (uint64_t)order_of(x[j]) << 32 | (uint32_t)(~(first + j * 64 + lane));
+    };
+    const bool listed = !equal && count <= kList;
+    if (listed) {
+      // what lies in the bin or above it; those of the bin that are not selected are taken out below
+      mask_of(masks, [&](int j) {
+        const float p = place_of(x[j]);
+        const bool in_or_above = x[j] > lo && p >= bin_from;
+        if (in_or_above && p < bin_to) add_to_list(j);
+        return in_or_above;
+      });
     }
-    __syncthreads();
-    const int bin = found[0];
-    int need = found[1];
-    const int count = bin < kBins ? hist[bin] : 0;
-    if (k == 0) {
-      least = INFINITY;
-    } else if (count <= kList) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j < per && x[j] > -INFINITY && bin_of(x[j]) == bin)
-          list[atomicAdd(&found[3], 1)] = (uint64_t)order_of(x[j]) << 32 | (uint32_t)~(first + j * 64 + lane);
-      __syncthreads();
-      if (tid < count) {
-        const uint64_t mine = list[tid];
-        int better = 0;
-        for (int i = 0; i < count; ++i) better += list[i] > mine;
-        if (better == need - 1) {
-          found[0] = (int)(mine >> 32);
-          found[1] = (int)~(uint32_t)mine;
+    while (!equal && count > kList) {
+      // the least and largest of them
+      uint32_t least_order = 0xffffffffu, most_order = 0;
+      each([&](int j) {
+        if (is_in(x[j])) {
+          const uint32_t u = order_of(x[j]);
+          least_order = u < least_order ? u : least_order;
+          most_order = u > most_order ? u : most_order;
         }
+      });
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t u = __shfl_xor(least_order, d), v = __shfl_xor(most_order, d);
+        least_order = u < least_order ? u : least_order;
+        most_order = v > most_order ? v : most_order;
       }
+      __syncthreads();  // the counts are read, and the bounds before
+      if (lane == 0) lows[wave] = __uint_as_float(least_order), highs[wave] = __uint_as_float(most_order);
+      hist[tid] = hist[tid + kSelectThreads] = 0;
       __syncthreads();
-      least = score_of((uint32_t)found[0]);
-      last = found[1];
+#pragma unroll
+      for (int w = 0; w < kSelectWaves; ++w) {
+        const uint32_t u = __float_as_uint(lows[w]), v = __float_as_uint(highs[w]);
+        least_order = u < least_order ? u : least_order;
+        most_order = v > most_order ? v : most_order;
+      }
+      from_order = __builtin_amdgcn_readfirstlane(least_order);
+      span = __builtin_amdgcn_readfirstlane(most_order) - from_order;
+      if (span == 0) {
+        equal = true;
+        break;
+      }
+      const int shift = span < (uint32_t)kBins ? 0 : 21 - __builtin_clz(span);  // span >> shift < kBins
+      each([&](int j) {
+        if (is_in(x[j])) atomicAdd(&hist[(order_of(x[j]) - from_order) >> shift], 1);
+      });
+      __syncthreads();
+      find(need);
+      need = found[1];
+      count = hist[found[0]];
+      const uint32_t begins = (uint32_t)found[0] << shift, width = (1u << shift) - 1;
+      span = span - begins < width ? span - begins : width;
+      from_order += begins;
+    }
+    if (equal) {
+      const float least = score_of(from_order);
+      mask_of(masks, [&](int j) { return x[j] > least; });
+      mask_of(ties, [&](int j) { return x[j] == least; });
+      tied = need;
+      __syncthreads();
     } else {
-      uint32_t prefix = 0;
-#pragma unroll 1
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        __syncthreads();  // the counts before are read
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (j < per && x[j] > -INFINITY && bin_of(x[j]) == bin) {
-            const uint32_t u = order_of(x[j]);
-            if (shift == 24 || u >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[u >> shift & 255], 1);
-          }
-        __syncthreads();
-        if (wave == 0) {  // a lane has four digits, from the highest on
-          const int d = 252 - 4 * lane;
-          const int c[4] = {hist[d + 3], hist[d + 2], hist[d + 1], hist[d]};
-          const int all = c[0] + c[1] + c[2] + c[3];
-          int before = wave_scan(all) - all;
-          if (before < need && before + all >= need) {
-            int i = 0;
-            while (before + c[i] < need) before += c[i++];
-            found[0] = d + 3 - i;
-            found[1] = need - before;
-          }
-        }
-        __syncthreads();
-        prefix |= (uint32_t)found[0] << shift;
-        need = found[1];
-      }
-      least = score_of(prefix);
-      // the position of the need-th score that is equal to it
-      int equal = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j < per) equal += __popcll(__ballot(x[j] == least));
-      if (lane == 0) sums[wave] = equal;
-      __syncthreads();
-      int before = 0;
-      for (int w = 0; w < wave; ++w) before += sums[w];
-      if (before < need && before + equal >= need) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (j < per) {
-            const uint64_t mask = __ballot(x[j] == least);
-            const int rank = before + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-            if (x[j] == least && rank == need - 1) found[2] = first + j * 64 + lane;
-            before += __popcll(mask);
-          }
+      if (!listed) {
+        mask_of(masks, [&](int j) {
+          if (is_in(x[j])) add_to_list(j);
+          return x[j] > lo && order_of(x[j]) >= from_order;
+        });
       }
       __syncthreads();
-      last = found[2];
+      // every wave compares with its share of them
+      for (int c = lane; c < count; c += 64) {
+        const uint64_t mine = list[c];
+        int better = 0;
+        for (int i = wave; i < count; i += kSelectWaves) better += list[i] > mine;
+        atomicAdd(&rank[c], better);
+      }
+      __syncthreads();
+      if (tid < count && rank[tid] >= need) {
+        const uint32_t i = ~(uint32_t)list[tid];
+        atomicAnd((uint32_t*)masks + 2 * (i >> 6) + (i >> 5 & 1), ~(1u << (i & 31)));
+      }
+      __syncthreads();
     }
   }
-  int count = 0;
+  auto scan = [&](int v, int* total) {  // exclusive
+    const int upto = wave_scan(v);
+    __syncthreads();  // what the sums held is read
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    int before = upto - v;
+    *total = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (j < per) count += __popcll(__ballot(x[j] > least || (x[j] == least && first + j * 64 + lane <= last)));
-  __syncthreads();  // what the sums held is read
-  if (lane == 0) sums[wave] = count;
-  __syncthreads();
-  int at = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kSelectWaves; ++w) {
-    if (w < wave) at += sums[w];
-    all += sums[w];
+    for (int w = 0; w < kSelectWaves; ++w) {
+      if (w < wave) before += sums[w];
+      *total += sums[w];
+    }
+    return before;
+  };
+  // a mask, or where there are fewer of them than threads an equal piece of one, to a thread
+  const int loads = kSelectWaves * blocks * kBlock, split = loads <= 64 ? 4 : loads <= 128 ? 3 : loads <= 256 ? 2 : loads <= 512 ? 1 : 0;
+  const int shift = (tid & ((1 << split) - 1)) * (64 >> split);
+  const bool has = tid >> split < loads;
+  const uint64_t piece = split ? (1ull << (64 >> split)) - 1 : ~0ull;
+  uint64_t mask = has ? masks[tid >> split] >> shift & piece : 0;
+  int all;
+  if (tied > 0) {
+    uint64_t tie = has ? ties[tid >> split] >> shift & piece : 0;
+    int room = tied - scan(__popcll(tie), &all);
+    for (; tie && room > 0; --room) {
+      mask |= tie & -tie;
+      tie &= tie - 1;
+    }
   }
+  int at = scan(__popcll(mask), &all);
   const int64_t to = whole ? row * a.k : (row * l.parts + part) * a.k;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (j < per) {
-      const int i = first + j * 64 + lane;
-      const bool is = x[j] > least || (x[j] == least && i <= last);
-      const uint64_t mask = __ballot(is);
-      if (is) {
-        const int64_t o = to + at + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-        const int32_t id = l.idx ? l.idx[row * l.n_in + begin + i] : (int32_t)(begin + i);
-        if (whole) {
-          a.topk[o] = id;
-        } else {
-          l.out[o] = x[j];
-          l.out_idx[o] = id;
-        }
-      }
-      at += __popcll(mask);
+  const int64_t in_row = begin + (tid >> split) * 64 + shift;
+  for (; mask; mask &= mask - 1, ++at) {
+    const int64_t i = in_row + __builtin_ctzll(mask);
+    const int32_t id = l.idx ? l.idx[row * l.n_in + i] : (int32_t)i;
+    if (whole) {
+      a.topk[to + at] = id;
+    } else {
+      l.out[to + at] = l.in[from * l.n_in + i];
+      l.out_idx[to + at] = id;
     }
+  }
   if (whole) {
     for (int i = all + tid; i < a.k; i += kSelectThreads) a.topk[to + i] = i < all + recent ? (int32_t)(m - recent + i - all) : -1;
   } else {
@@ -265,9 +350,9 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(SelectArgs a, Se
   }
 }
 
-template <int kPer>
+template <int kPer, int kBlock>
 void launch(const SelectArgs& a, const SelectLevel& l, hipStream_t s) {
-  hipLaunchKernelGGL(select_kernel<kPer>, dim3((uint32_t)((int64_t)a.rows * l.parts)), dim3(kSelectThreads), 0, s, a, l);
+  hipLaunchKernelGGL((select_kernel<kPer, kBlock>), dim3((uint32_t)((int64_t)a.rows * l.parts)), dim3(kSelectThreads), 0, s, a, l);
 }
 
 // Positions to a workgroup in a launch over rows of n > kMost: as few as leave the next launch one workgroup to a row, where
@@ -301,7 +386,7 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
     l.parts = (int32_t)(left / a.k);
     l.out = (float*)work;
     l.out_idx = (int32_t*)(work + (uint64_t)a.rows * left * 4);
-    launch<kMost / kSelectThreads>(a, l, s);
+    launch<kMost / kSelectThreads, 8>(a, l, s);
     work += (uint64_t)a.rows * left * 8;
     l.in = l.out;
     l.idx = l.out_idx;
@@ -312,9 +397,9 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
   l.out = nullptr;
   l.out_idx = nullptr;
   const int64_t per = (l.n_in + kSelectThreads - 1) / kSelectThreads;
-  if (per <= 4) launch<4>(a, l, s);
-  else if (per <= 16) launch<16>(a, l, s);
-  else launch<48>(a, l, s);
+  if (per <= 4) launch<4, 4>(a, l, s);
+  else if (per <= 16) launch<16, 8>(a, l, s);
+  else launch<48, 8>(a, l, s);
   return hipGetLastError();
 }
 
