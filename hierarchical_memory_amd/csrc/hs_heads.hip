@@ -24,12 +24,13 @@ enum Mode { kPairs, kInLane, kTwoLanes, kAnywhere, kStill };
 
 struct HeadPlan {
   int32_t mode;
-  uint32_t magic;  // ceil(2^32 / heads): (i * magic) >> 32 = i / heads for i < 2^16
+  uint32_t magic, pair_magic;  // ceil(2^32 / heads), ceil(2^32 / (rope / 2)): (i * magic) >> 32 = i / heads for i < 2^16
+  int32_t span;    // heads of a workgroup (its first threads'; all of its threads work out turns)
   int32_t tokens;  // most tokens of a workgroup
 };
 
 // Waves to a SIMD: a wave has its C kilobytes on their way, so that four of them keep the memory busy.
-constexpr int kWavesOf(int C) { return C <= 2 ? 6 : C <= 5 ? 4 : 3; }
+constexpr int kWavesOf(int C) { return C <= 1 ? 6 : C <= 2 ? 5 : C <= 4 ? 4 : C <= 6 ? 3 : 2; }
 
 template <class T>
 __device__ __forceinline__ T quad_sum(T v) {
@@ -56,13 +57,14 @@ __device__ __forceinline__ void turn_in_lane(float (&y)[C][8], int piece0, int q
   }
 }
 
-// C: blocks of 32 values of a head.
-template <int C, Out kOut>
+// C: blocks of 32 values of a head. kAll: with the ways that few heads are rotated in, halves of other than 16 or 32 values (they
+// take registers: 8192 tokens x 32 heads x 128 values in 8 bits 29 us with them in one kernel, 24 without).
+template <int C, Out kOut, bool kAll>
 __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadArgs a, HeadPlan plan) {
   constexpr bool kCache = kOut == kCache8 || kOut == kCache4;
   __shared__ __align__(16) uint16_t weight[32 * C], bias[32 * C];
   extern __shared__ __align__(16) float2 turns[];  // [tokens][rope / 2] (cosine, sine), then [heads of the workgroup][rope] values
-  const int tid = threadIdx.x, lane = tid & 3, span = blockDim.x / 4;
+  const int tid = threadIdx.x, lane = tid & 3, span = plan.span;
   const int P = a.rope / 2, q = a.rope / 16, piece0 = lane - a.rope_at / 8;
   const bool rotate = plan.mode != kStill;
   const int64_t units = (int64_t)a.n * a.heads;
@@ -94,8 +96,8 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
     if (rotate) {
       if (u0 != (int64_t)blockIdx.x * span) __syncthreads();  // the turns before are read
       const int tokens = a.heads == 1 ? mine : (int)__umulhi((uint32_t)(h0 + mine - 1), plan.magic) + 1;
-      for (int i = tid; i < tokens * P; i += blockDim.x) {
-        const int k = i / P, pair = i - k * P, x = a.pos[t0 + k];
+      for (int i = tid; i < tokens * P; i += kHeadThreads) {
+        const int k = (int)__umulhi((uint32_t)i, plan.pair_magic), pair = i - k * P, x = a.pos[t0 + k];
         // the angle in turns, in 64 bits, less its whole turns: what is left of it is exact enough in 32
         const double turn = (double)(x < 0 ? 0 : x) * (a.freqs[pair] * 0.15915494309189535);
         float s, c;
@@ -150,9 +152,11 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
         }
         d = 1.0 / sqrt(quad_sum(d) / (32 * C) + (double)a.eps);
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[i][e] = (float)(((double)(float)again[32 * i + e] - m) * d);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -184,7 +188,7 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
           __builtin_amdgcn_sched_barrier(0);
         }
       } else if (plan.mode == kInLane) {
-        if (q == 4) turn_in_lane<C, 1>(y, piece0, q, cs);
+        if (!kAll || q == 4) turn_in_lane<C, 1>(y, piece0, q, cs);
         else if (q == 8) turn_in_lane<C, 2>(y, piece0, q, cs);
         else if (q == 12) turn_in_lane<C, 3>(y, piece0, q, cs);
         else turn_in_lane<C, 4>(y, piece0, q, cs);
@@ -203,7 +207,7 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-      } else {
+      } else if constexpr (kAll) {
         float* part = (float*)(turns + plan.tokens * P) + u * a.rope;  // (the four lanes are of one wave: its LDS accesses stay in order)
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -211,6 +215,7 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
           if (p >= 0 && p < 2 * q)
 #pragma unroll
             for (int e = 0; e < 8; ++e) part[8 * p + e] = y[i][e];
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -320,13 +325,23 @@ hipError_t launch(const HeadArgs& a, hipStream_t s) {
   HeadPlan plan{};
   plan.mode = !a.freqs ? kStill : !a.halves ? kPairs : q % 4 == 0 ? kInLane : q == 2 && a.rope_at % 32 == 0 ? kTwoLanes : kAnywhere;
   plan.magic = a.heads == 1 ? 0 : (uint32_t)(((1ull << 32) + a.heads - 1) / a.heads);
-  const int threads = plan.mode == kAnywhere ? 64 : kHeadThreads, span = threads / 4;
-  plan.tokens = a.heads == 1 ? span : (a.heads + span - 2) / a.heads + 1;
+  plan.pair_magic = a.rope ? (uint32_t)(((1ull << 32) + a.rope / 2 - 1) / (a.rope / 2)) : 0;
+  // 64 heads to a workgroup (16 where they exchange values through LDS), or as few as leave each thread one turn where there are
+  // not 512 workgroups: with single heads, the keys, a workgroup has a token for each of them (256 keys: 6.8 us with 64, 6.3 with 4;
+  // 256 tokens with 32 heads: 4.6 with 64, 5.3 with 16)
+  int span = plan.mode == kAnywhere ? 16 : kHeadThreads / 4;
+  auto tokens = [&] { return a.heads == 1 ? span : (a.heads + span - 2) / a.heads + 1; };
+  while (plan.mode != kStill && span > 4 && units < (int64_t)span * 512 && tokens() * (a.rope / 2) > kHeadThreads) span /= 2;
+  plan.span = span;
+  plan.tokens = tokens();
   const size_t lds = plan.mode == kStill ? 0 : (size_t)plan.tokens * a.rope / 2 * sizeof(float2) +
                                                    (plan.mode == kAnywhere ? (size_t)span * a.rope * sizeof(float) : 0);
   const int64_t need = (units + span - 1) / span;
-  hipLaunchKernelGGL((heads_kernel<C, kOut>), dim3((uint32_t)(need < kMostHeadBlocks ? need : kMostHeadBlocks)), dim3(threads), lds, s,
-                     a, plan);
+  const dim3 grid((uint32_t)(need < kMostHeadBlocks ? need : kMostHeadBlocks));
+  if (plan.mode == kAnywhere || (plan.mode == kInLane && q > 4))
+    hipLaunchKernelGGL((heads_kernel<C, kOut, true>), grid, dim3(kHeadThreads), lds, s, a, plan);
+  else
+    hipLaunchKernelGGL((heads_kernel<C, kOut, false>), grid, dim3(kHeadThreads), lds, s, a, plan);
   return hipGetLastError();
 }
 

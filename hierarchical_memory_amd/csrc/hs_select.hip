@@ -4,7 +4,7 @@
 // a mask of each such load, and a thread then writes the positions of one mask: passes over the registers are unrolled code that
 // runs once and waits for its own instructions, and three of them are enough (with two more, to count and to write by ballots,
 // 256 rows of 40960 took 31 us). The k-th best score is found without a sort. It is no lower than the lowest of the threads' own
-// best (or second best) scores, where that makes k of them; what lies above is counted in 2048 bins, even in value (which keeps a
+// best scores (or second best, and so on: as many as make k); what lies above is counted in bins, even in value (which keeps a
 // wave's counts apart, where the bits of the scores would share few bins), and the scores of the one bin that the k-th lies in,
 // some dozens, are ranked against each other with their positions. A bin of more than kList (few different scores, or outliers
 // that stretch the range) is divided further, by the scores' bits, until kList are left or all are equal; the first of the
@@ -17,12 +17,12 @@ namespace hs {
 
 namespace {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectWaves = kSelectThreads / 64;
-constexpr int kBins = 2 * kSelectThreads;
+constexpr int kSelectThreads = 1024;         // of a workgroup, for rows of more than kShort
+constexpr int kShortThreads = 512;
+constexpr int kShort = 8 * kShortThreads;
 constexpr int kList = 512;                   // scores of a bin that are ranked against each other
 constexpr int kMost = 48 * kSelectThreads;   // positions of a workgroup
-constexpr int kLeastPart = 8192;             // of a part of a longer row
+constexpr int kMiddle = 16 * kSelectThreads; // up to which a kernel that takes half of the registers is used
 
 struct SelectLevel {
   const float* in;      // rows of n_in scores
@@ -61,14 +61,17 @@ __device__ __forceinline__ float wave_reduce(float v, Op op) {
 }
 
 // kPer: most scores of a thread, kBlock of them in a block: a workgroup passes over as many blocks as its part has.
-template <int kPer, int kBlock>
-__global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_kernel(SelectArgs a, SelectLevel l) {
+template <int kThreads, int kPer>
+__global__ __launch_bounds__(kThreads, kPer <= 16 ? 8 : 4) void select_kernel(SelectArgs a, SelectLevel l) {
+  constexpr int kWaves = kThreads / 64, kBins = 2 * kThreads, kBlock = 8;
+  constexpr int kBest = 2048 / kThreads;  // of a thread's scores, for the bound
   __shared__ int hist[kBins];
   __shared__ uint64_t list[kList];
   __shared__ int rank[kList];
-  __shared__ uint64_t masks[kSelectWaves * kPer], ties[kSelectWaves * kPer];  // of the loads, in the order of the positions
-  __shared__ int sums[kSelectWaves], found[4];
-  __shared__ float lows[kSelectWaves], highs[kSelectWaves];
+  __shared__ uint64_t masks[kWaves * kPer], ties[kWaves * kPer];  // of the loads, in the order of the positions
+  __shared__ int sums[kWaves], tie_sums[kWaves], taken_sums[kWaves], found[4];
+  __shared__ uint16_t chosen[kMaxTopK];
+  __shared__ float lows[kWaves], highs[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t row = blockIdx.x / l.parts;
   const int part = (int)(blockIdx.x % l.parts);
@@ -88,7 +91,7 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
   const int recent = m < a.recent ? (int)m : a.recent, k = a.k - recent;
   const int64_t rivals = l.idx ? l.n_in : m - recent, begin = part * l.part;
   const int n = (int)(rivals <= begin ? 0 : rivals - begin < l.part ? rivals - begin : l.part);
-  const int blocks = (n + kSelectThreads * kBlock - 1) / (kSelectThreads * kBlock);
+  const int blocks = (n + kThreads * kBlock - 1) / (kThreads * kBlock);
   const int first = wave * blocks * kBlock * 64;  // of the wave
   float x[kPer];
   // f(j) for the wave's loads, in their order
@@ -118,24 +121,29 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
         }
       }
   }
-  hist[tid] = hist[tid + kSelectThreads] = 0;
-  if (tid < kList) rank[tid] = 0;
+  hist[tid] = hist[tid + kThreads] = 0;
+  for (int i = tid; i < kList; i += kThreads) rank[i] = 0;
   if (tid == 0) found[3] = 0;
-  // a NaN becomes -infinity: what is never selected has one form, and no comparison below meets a NaN
-  float best = -INFINITY, second = -INFINITY;
+  // (a median leaves out a NaN, and is one instruction where the larger of two would be two)
+  float best[kBest];
+#pragma unroll
+  for (int i = 0; i < kBest; ++i) best[i] = -INFINITY;
   each([&](int j) {
-    x[j] = x[j] == x[j] ? x[j] : -INFINITY;
-    second = __builtin_amdgcn_fmed3f(x[j], best, second);
-    best = fmaxf(best, x[j]);
+#pragma unroll
+    for (int i = kBest - 1; i >= 0; --i) best[i] = __builtin_amdgcn_fmed3f(x[j], i ? best[i - 1] : INFINITY, best[i]);
   });
+  float bound = -INFINITY;  // as many of each thread's as make k
+#pragma unroll
+  for (int i = 0; i < kBest; ++i)
+    if (k > i * kThreads && k <= (i + 1) * kThreads) bound = best[i];
   const auto lesser = [](float u, float v) { return fminf(u, v); };
   const auto larger = [](float u, float v) { return fmaxf(u, v); };
-  float hi = wave_reduce(best, larger);
-  float lo = wave_reduce(k <= kSelectThreads ? best : k <= 2 * kSelectThreads ? second : -INFINITY, lesser);
+  float hi = wave_reduce(best[0], larger);
+  float lo = wave_reduce(bound, lesser);
   if (lane == 0) lows[wave] = lo, highs[wave] = hi;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSelectWaves; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     lo = fminf(lo, lows[w]);
     hi = fmaxf(hi, highs[w]);
   }
@@ -152,10 +160,12 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
   int tied = 0;        // of the equal scores in `ties`, those that are selected
   bool every = false;  // what may be selected is
   if (lo == -INFINITY) {
-    // too few scores for that bound: the lowest that may be selected, and how many may
+    // too few scores for that bound: the lowest that may be selected, and how many may (a NaN becomes -infinity, so that no ballot
+    // meets one)
     int valid = 0;
     lo = INFINITY;
     each([&](int j) {
+      x[j] = x[j] == x[j] ? x[j] : -INFINITY;
       lo = fminf(lo, x[j] > -INFINITY ? x[j] : INFINITY);
       valid += __popcll(__ballot(x[j] > -INFINITY));
     });
@@ -165,7 +175,7 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
     __syncthreads();
     valid = 0;
 #pragma unroll
-    for (int w = 0; w < kSelectWaves; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       lo = fminf(lo, lows[w]);
       valid += sums[w];
     }
@@ -179,7 +189,7 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
     __syncthreads();
     int before = upto - both, all = 0;
 #pragma unroll
-    for (int w = 0; w < kSelectWaves; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       if (w < wave) before += sums[w];
       all += sums[w];
     }
@@ -246,10 +256,10 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
       }
       __syncthreads();  // the counts are read, and the bounds before
       if (lane == 0) lows[wave] = __uint_as_float(least_order), highs[wave] = __uint_as_float(most_order);
-      hist[tid] = hist[tid + kSelectThreads] = 0;
+      hist[tid] = hist[tid + kThreads] = 0;
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kSelectWaves; ++w) {
+      for (int w = 0; w < kWaves; ++w) {
         const uint32_t u = __float_as_uint(lows[w]), v = __float_as_uint(highs[w]);
         least_order = u < least_order ? u : least_order;
         most_order = v > most_order ? v : most_order;
@@ -260,7 +270,7 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
         equal = true;
         break;
       }
-      const int shift = span < (uint32_t)kBins ? 0 : 21 - __builtin_clz(span);  // span >> shift < kBins
+      const int shift = span < (uint32_t)kBins ? 0 : __builtin_clz(kBins - 1) - __builtin_clz(span);  // span >> shift < kBins
       each([&](int j) {
         if (is_in(x[j])) atomicAdd(&hist[(order_of(x[j]) - from_order) >> shift], 1);
       });
@@ -290,33 +300,33 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
       for (int c = lane; c < count; c += 64) {
         const uint64_t mine = list[c];
         int better = 0;
-        for (int i = wave; i < count; i += kSelectWaves) better += list[i] > mine;
+        for (int i = wave; i < count; i += kWaves) better += list[i] > mine;
         atomicAdd(&rank[c], better);
       }
       __syncthreads();
-      if (tid < count && rank[tid] >= need) {
-        const uint32_t i = ~(uint32_t)list[tid];
-        atomicAnd((uint32_t*)masks + 2 * (i >> 6) + (i >> 5 & 1), ~(1u << (i & 31)));
-      }
+      for (int c = tid; c < count; c += kThreads)
+        if (rank[c] >= need) {
+          const uint32_t i = ~(uint32_t)list[c];
+          atomicAnd((uint32_t*)masks + 2 * (i >> 6) + (i >> 5 & 1), ~(1u << (i & 31)));
+        }
       __syncthreads();
     }
   }
-  auto scan = [&](int v, int* total) {  // exclusive
+  auto scan = [&](int v, int* sums, int* total) {  // exclusive
     const int upto = wave_scan(v);
-    __syncthreads();  // what the sums held is read
     if (lane == 63) sums[wave] = upto;
     __syncthreads();
     int before = upto - v;
     *total = 0;
 #pragma unroll
-    for (int w = 0; w < kSelectWaves; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       if (w < wave) before += sums[w];
       *total += sums[w];
     }
     return before;
   };
   // a mask, or where there are fewer of them than threads an equal piece of one, to a thread
-  const int loads = kSelectWaves * blocks * kBlock, split = loads <= 64 ? 4 : loads <= 128 ? 3 : loads <= 256 ? 2 : loads <= 512 ? 1 : 0;
+  const int loads = kWaves * blocks * kBlock, split = loads <= kThreads / 8 ? 3 : loads <= kThreads / 4 ? 2 : loads <= kThreads / 2 ? 1 : 0;
   const int shift = (tid & ((1 << split) - 1)) * (64 >> split);
   const bool has = tid >> split < loads;
   const uint64_t piece = split ? (1ull << (64 >> split)) - 1 : ~0ull;
@@ -324,53 +334,54 @@ __global__ __launch_bounds__(kSelectThreads, kPer <= 16 ? 8 : 4) void select_ker
   int all;
   if (tied > 0) {
     uint64_t tie = has ? ties[tid >> split] >> shift & piece : 0;
-    int room = tied - scan(__popcll(tie), &all);
+    int room = tied - scan(__popcll(tie), tie_sums, &all);
     for (; tie && room > 0; --room) {
       mask |= tie & -tie;
       tie &= tie - 1;
     }
   }
-  int at = scan(__popcll(mask), &all);
+  int at = scan(__popcll(mask), taken_sums, &all);
+  // (through LDS, so that a thread's positions need not wait for each other's loads, and stores are whole)
+  const int in_part = (tid >> split) * 64 + shift;
+  for (; mask; mask &= mask - 1) chosen[at++] = (uint16_t)(in_part + __builtin_ctzll(mask));
+  __syncthreads();
   const int64_t to = whole ? row * a.k : (row * l.parts + part) * a.k;
-  const int64_t in_row = begin + (tid >> split) * 64 + shift;
-  for (; mask; mask &= mask - 1, ++at) {
-    const int64_t i = in_row + __builtin_ctzll(mask);
+  for (int o = tid; o < all; o += kThreads) {
+    const int64_t i = begin + chosen[o];
     const int32_t id = l.idx ? l.idx[row * l.n_in + i] : (int32_t)i;
     if (whole) {
-      a.topk[to + at] = id;
+      a.topk[to + o] = id;
     } else {
-      l.out[to + at] = l.in[from * l.n_in + i];
-      l.out_idx[to + at] = id;
+      l.out[to + o] = l.in[from * l.n_in + i];
+      l.out_idx[to + o] = id;
     }
   }
   if (whole) {
-    for (int i = all + tid; i < a.k; i += kSelectThreads) a.topk[to + i] = i < all + recent ? (int32_t)(m - recent + i - all) : -1;
+    for (int i = all + tid; i < a.k; i += kThreads) a.topk[to + i] = i < all + recent ? (int32_t)(m - recent + i - all) : -1;
   } else {
-    for (int i = all + tid; i < a.k; i += kSelectThreads) l.out[to + i] = -INFINITY;
+    for (int i = all + tid; i < a.k; i += kThreads) l.out[to + i] = -INFINITY;
   }
 }
 
-template <int kPer, int kBlock>
+template <int kThreads, int kPer>
 void launch(const SelectArgs& a, const SelectLevel& l, hipStream_t s) {
-  hipLaunchKernelGGL((select_kernel<kPer, kBlock>), dim3((uint32_t)((int64_t)a.rows * l.parts)), dim3(kSelectThreads), 0, s, a, l);
+  hipLaunchKernelGGL((select_kernel<kThreads, kPer>), dim3((uint32_t)((int64_t)a.rows * l.parts)), dim3(kThreads), 0, s, a, l);
 }
 
-// Positions to a workgroup in a launch over rows of n > kMost: as few as leave the next launch one workgroup to a row, where
-// there are such.
-int64_t part_of(int64_t n, int k) {
-  const int64_t parts = kMost / k, part = (n + parts - 1) / parts;
-  return part < kLeastPart ? kLeastPart : part < kMost ? part : kMost;
-}
-
-// Scores of a row that it leaves.
-int64_t left_of(int64_t n, int k) { return (n + part_of(n, k) - 1) / part_of(n, k) * k; }
+// The part into which a launch cuts rows of more than kMost: one that leaves an eighth of them and runs two workgroups to a unit, or,
+// where that would leave more than a quarter, the longest (2 rows of 1 M, k 2048: 62 parts, then 8, then one, 33 us; in parts of 41 K
+// 48).
+int64_t part_of(int k) { return 4 * k <= kMiddle ? kMiddle : kMost; }
 
 }  // namespace
 
 // Every launch but the last leaves k scores and positions of each part.
 uint64_t select_work_bytes(int rows, int64_t columns, int k) {
   uint64_t bytes = 0;
-  for (int64_t n = columns; n > kMost; n = left_of(n, k)) bytes += (uint64_t)rows * left_of(n, k) * 8;
+  for (int64_t n = columns; n > kMost;) {
+    n = (n + part_of(k) - 1) / part_of(k) * k;
+    bytes += (uint64_t)rows * n * 8;
+  }
   return (bytes + 15) & ~15ull;
 }
 
@@ -380,27 +391,23 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
   l.in = a.scores;
   l.n_in = a.columns;
   char* work = a.work;
-  while (l.n_in > kMost) {
-    const int64_t left = left_of(l.n_in, a.k);
-    l.part = part_of(l.n_in, a.k);
-    l.parts = (int32_t)(left / a.k);
-    l.out = (float*)work;
+  for (;;) {
+    const bool last = l.n_in <= kMost;
+    l.part = last ? kMost : part_of(a.k);
+    l.parts = (int32_t)((l.n_in + l.part - 1) / l.part);
+    if (l.parts == 0) l.parts = 1;
+    const int64_t left = (int64_t)l.parts * a.k, most = l.n_in < l.part ? l.n_in : l.part;  // of a workgroup
+    l.out = last ? nullptr : (float*)work;
     l.out_idx = (int32_t*)(work + (uint64_t)a.rows * left * 4);
-    launch<kMost / kSelectThreads, 8>(a, l, s);
+    if (most <= kShort) launch<kShortThreads, kShort / kShortThreads>(a, l, s);
+    else if (most <= kMiddle) launch<kSelectThreads, kMiddle / kSelectThreads>(a, l, s);
+    else launch<kSelectThreads, kMost / kSelectThreads>(a, l, s);
+    if (last) return hipGetLastError();
     work += (uint64_t)a.rows * left * 8;
     l.in = l.out;
     l.idx = l.out_idx;
     l.n_in = left;
   }
-  l.part = kMost;
-  l.parts = 1;
-  l.out = nullptr;
-  l.out_idx = nullptr;
-  const int64_t per = (l.n_in + kSelectThreads - 1) / kSelectThreads;
-  if (per <= 4) launch<4, 4>(a, l, s);
-  else if (per <= 16) launch<16, 8>(a, l, s);
-  else launch<48, 8>(a, l, s);
-  return hipGetLastError();
 }
 
 }  // namespace hs

@@ -642,14 +642,15 @@ def key_parts(cfg: HsConfig, key: HsKeyFormat, keys):
 
 def _strides(name: str, x, dim: int):
     """(token, head) strides of x [n, heads, dim], those of a dimension of one element set to what packed ones have."""
-    if x.dim() != 3 or x.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [n, heads, {dim}], got {list(x.shape)}")
-    n, heads, _ = x.shape
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"{name} must have shape [n, heads, {dim}], got {list(shape)}")
     token, head, one = x.stride()
     if one != 1:
         raise ValueError(f"{name} must have contiguous heads")
-    head = head if heads > 1 else dim
-    return (token if n > 1 else max(dim, heads * head)), head
+    if shape[1] == 1:
+        head = dim
+    return (token if shape[0] > 1 else max(dim, shape[1] * head)), head
 
 
 def hs_norm_rotate(ctx, fmt: HsHeadFormat, x, weight, bias, freqs, pos, o, scales=None, stream=None) -> None:
@@ -657,29 +658,27 @@ def hs_norm_rotate(ctx, fmt: HsHeadFormat, x, weight, bias, freqs, pos, o, scale
     None; freqs: float64 [rope / 2] or None; pos: int32 [n] (None: no rotation, no token skipped); o: bf16 [n, heads, dim],
     strided like x (x itself for a call in place), or, with scales (uint8 [n, heads, dim / 32]), float8_e4m3fn."""
     t = _t()
-    bf16 = t.bfloat16
+    bf16, f64, u8 = t.bfloat16, t.float64, t.uint8
     D = fmt.dim
-    for name, v in (("x", x), ("o", o)):
-        if v is None:
-            raise ValueError(f"{name} must not be None")
+    if x is None or o is None:
+        raise ValueError(f"{'x' if x is None else 'o'} must not be None")
     if x.dtype is not bf16:
         raise ValueError(f"x must be a {bf16} tensor, got {x.dtype}")
     (xt, xh), (ot, oh) = _strides("x", x, D), _strides("o", o, D)
-    n, heads, _ = x.shape
     if o.shape != x.shape:
         raise ValueError(f"o must have shape {list(x.shape)}, got {list(o.shape)}")
+    n, heads, _ = x.shape
     dev = x.get_device()
     kind = bf16 if scales is None else t.float8_e4m3fn
-    if not (o.dtype is kind and o.get_device() == dev and (scales is None or o.is_contiguous())
+    if not (o.dtype is kind and o.get_device() == dev
+            and (scales is None or (_fine(scales, u8, (n, heads, D // 32), dev) and o.is_contiguous()))
             and (weight is None or _fine(weight, bf16, (D,), dev)) and (bias is None or _fine(bias, bf16, (D,), dev))
-            and (freqs is None or _fine(freqs, t.float64, (fmt.rope // 2,), dev))
-            and (pos is None or _fine(pos, t.int32, (n,), dev))
-            and (scales is None or _fine(scales, t.uint8, (n, heads, D // 32), dev))
+            and (freqs is None or _fine(freqs, f64, (fmt.rope // 2,), dev)) and (pos is None or _fine(pos, t.int32, (n,), dev))
             and dev >= 0 and dev == t._C._cuda_getDevice()):
         _refuse(_current(dev), ("x", x[:0], None, None, False), ("weight", weight, bf16, (D,), True),
-                ("bias", bias, bf16, (D,), True), ("freqs", freqs, t.float64, (fmt.rope // 2,), True),
+                ("bias", bias, bf16, (D,), True), ("freqs", freqs, f64, (fmt.rope // 2,), True),
                 ("pos", pos, t.int32, (n,), True), ("o", o[:0] if scales is None else o, kind, None, False),
-                ("scales", scales, t.uint8, (n, heads, D // 32), True))
+                ("scales", scales, u8, (n, heads, D // 32), True))
     _check(lib().hs_norm_rotate(ctx, ctypes.byref(fmt), x.data_ptr(), xt, xh, heads, _at(weight), _at(bias), _at(freqs),
                                 _at(pos), n, o.data_ptr(), ot, oh, _at(scales), _raw_stream(stream, dev)))
 
