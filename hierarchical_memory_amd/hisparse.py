@@ -664,20 +664,24 @@ def hs_norm_rotate(ctx, fmt: HsHeadFormat, x, weight, bias, freqs, pos, o, scale
         raise ValueError(f"{'x' if x is None else 'o'} must not be None")
     if x.dtype is not bf16:
         raise ValueError(f"x must be a {bf16} tensor, got {x.dtype}")
-    (xt, xh), (ot, oh) = _strides("x", x, D), _strides("o", o, D)
-    if o.shape != x.shape:
-        raise ValueError(f"o must have shape {list(x.shape)}, got {list(o.shape)}")
-    n, heads, _ = x.shape
+    xt, xh = _strides("x", x, D)
+    n, heads, _ = shape = x.shape
+    if o.shape != shape:
+        raise ValueError(f"o must have shape {list(shape)}, got {list(o.shape)}")
     dev = x.get_device()
-    kind = bf16 if scales is None else t.float8_e4m3fn
-    if not (o.dtype is kind and o.get_device() == dev
-            and (scales is None or (_fine(scales, u8, (n, heads, D // 32), dev) and o.is_contiguous()))
-            and (weight is None or _fine(weight, bf16, (D,), dev)) and (bias is None or _fine(bias, bf16, (D,), dev))
-            and (freqs is None or _fine(freqs, f64, (fmt.rope // 2,), dev)) and (pos is None or _fine(pos, t.int32, (n,), dev))
-            and dev >= 0 and dev == t._C._cuda_getDevice()):
+    if scales is None:
+        ot, oh = _strides("o", o, D)
+        fine = o.dtype is bf16
+    else:
+        ot, oh = heads * D, D
+        fine = (o.dtype is t.float8_e4m3fn and o.is_contiguous() and _fine(scales, u8, (n, heads, D // 32), dev))
+    if not (fine and o.get_device() == dev and (freqs is None or _fine(freqs, f64, (fmt.rope // 2,), dev))
+            and (pos is None or _fine(pos, t.int32, (n,), dev)) and (weight is None or _fine(weight, bf16, (D,), dev))
+            and (bias is None or _fine(bias, bf16, (D,), dev)) and dev >= 0 and dev == t._C._cuda_getDevice()):
         _refuse(_current(dev), ("x", x[:0], None, None, False), ("weight", weight, bf16, (D,), True),
                 ("bias", bias, bf16, (D,), True), ("freqs", freqs, f64, (fmt.rope // 2,), True),
-                ("pos", pos, t.int32, (n,), True), ("o", o[:0] if scales is None else o, kind, None, False),
+                ("pos", pos, t.int32, (n,), True),
+                ("o", o[:0] if scales is None else o, bf16 if scales is None else t.float8_e4m3fn, None, False),
                 ("scales", scales, u8, (n, heads, D // 32), True))
     _check(lib().hs_norm_rotate(ctx, ctypes.byref(fmt), x.data_ptr(), xt, xh, heads, _at(weight), _at(bias), _at(freqs),
                                 _at(pos), n, o.data_ptr(), ot, oh, _at(scales), _raw_stream(stream, dev)))
