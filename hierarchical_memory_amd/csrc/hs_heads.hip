@@ -76,11 +76,12 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
   for (int64_t u0 = (int64_t)blockIdx.x * span; u0 < units; u0 += (int64_t)gridDim.x * span) {
     const int64_t t0 = a.heads == 1 ? u0 : u0 / a.heads;
     const int h0 = (int)(u0 - t0 * a.heads), mine = (int)(units - u0 < span ? units - u0 : span);
-    const int u = tid >> 2, local = h0 + (u < mine ? u : mine - 1);  // (lanes behind the last head repeat it, and store nothing)
+    const bool has = tid >> 2 < mine;
+    const int u = has ? tid >> 2 : mine - 1, local = h0 + u;  // (lanes behind the last head repeat it, and store nothing)
     const int tok = a.heads == 1 ? local : (int)__umulhi((uint32_t)local, plan.magic), h = local - tok * a.heads;
     const int64_t t = t0 + tok;
     const int position = a.pos ? a.pos[t] : 0;
-    bool there = u < mine && position >= 0;
+    bool there = has && position >= 0;
     const uint16_t* in = a.x + t * a.x_stride + h * a.x_head_stride + 8 * lane;
     bf8 v[C];
 #pragma unroll
