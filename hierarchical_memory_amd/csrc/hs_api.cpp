@@ -1008,7 +1008,8 @@ int hs_norm_rotate(hs_ctx* ctx, const hs_head_format* fmt, const void* d_x, int6
     return fail(HS_E_INVALID, "o's strides must be multiples of 8 and at least %d (got %lld and %lld)", fmt->dim,
                 (long long)o_stride, (long long)o_head_stride);
   }
-  if (!aligned(d_x, 16) || !aligned(d_o, 16)) return fail(HS_E_INVALID, "x and o must be 16-byte aligned");
+  if (!aligned(d_x, 16) || !aligned(d_o, 16) || !aligned(d_o_scales, 4))
+    return fail(HS_E_INVALID, "x and o must be 16-byte aligned, o's scales 4-byte aligned");
   a.heads = heads;
   a.n = n_tokens;
   a.x_stride = x_stride;

@@ -482,7 +482,7 @@ typedef struct hs_head_format {
  *   d_o        d_o_scales NULL: bf16, addressed as d_x is by o_stride and o_head_stride (multiples of 8, >= dim; no two heads
  *              may overlap). It may be d_x with the same strides; any other overlap is not allowed
  *              else: e4m3 [n_tokens][heads][dim] (o_stride heads * dim, o_head_stride dim). 16-byte aligned
- *   d_o_scales e8m0 [n_tokens][heads][dim / 32], or NULL
+ *   d_o_scales e8m0 [n_tokens][heads][dim / 32], 4-byte aligned, or NULL
  * heads: 1 .. 512; n_tokens from 0 to 2^30.
  */
 int hs_norm_rotate(hs_ctx* ctx, const hs_head_format* fmt, const void* d_x, int64_t x_stride, int64_t x_head_stride,
