@@ -13,6 +13,8 @@
 // launch; ties stay with the lowest positions, as every launch keeps the order.
 #include "hs_index.h"
 
+#include <algorithm>
+
 namespace hs {
 
 namespace {
@@ -29,6 +31,7 @@ struct SelectLevel {
   const int32_t* idx;   // their positions, or nullptr (first launch: their places)
   int64_t n_in;
   int64_t part;         // of a row, to a workgroup
+  int64_t row0;         // of the launch
   int32_t parts;
   float* out;           // not the last launch: [row][parts][k] scores, -inf behind the selected, and
   int32_t* out_idx;     // their positions
@@ -73,7 +76,7 @@ __global__ __launch_bounds__(kThreads, kPer <= 16 ? 8 : 4) void select_kernel(Se
   __shared__ uint16_t chosen[kMaxTopK];
   __shared__ float lows[kWaves], highs[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t row = blockIdx.x / l.parts;
+  const int64_t row = l.row0 + blockIdx.x / l.parts;
   const int part = (int)(blockIdx.x % l.parts);
   const bool whole = l.out == nullptr;
   // the positions of the row's token, those that compete, and how many of them are selected
@@ -364,8 +367,12 @@ __global__ __launch_bounds__(kThreads, kPer <= 16 ? 8 : 4) void select_kernel(Se
 }
 
 template <int kThreads, int kPer>
-void launch(const SelectArgs& a, const SelectLevel& l, hipStream_t s) {
-  hipLaunchKernelGGL((select_kernel<kThreads, kPer>), dim3((uint32_t)((int64_t)a.rows * l.parts)), dim3(kThreads), 0, s, a, l);
+void launch(const SelectArgs& a, SelectLevel l, hipStream_t s) {
+  const int64_t most = std::max<int64_t>(1, (1 << 21) / l.parts);  // rows of a launch (which ends below 2^32 threads)
+  for (l.row0 = 0; l.row0 < a.rows; l.row0 += most) {
+    const int64_t rows = std::min<int64_t>(most, a.rows - l.row0);
+    hipLaunchKernelGGL((select_kernel<kThreads, kPer>), dim3((uint32_t)(rows * l.parts)), dim3(kThreads), 0, s, a, l);
+  }
 }
 
 // The part into which a launch cuts rows of more than kMost: one that leaves an eighth of them and runs two workgroups to a unit, or,
