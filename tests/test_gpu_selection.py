@@ -127,6 +127,47 @@ def test_heads_sizes(n, heads, dim, bits):
         assert torch.equal(g[:, h:h + 1].view(torch.uint8), m.view(torch.uint8))
 
 
+TURNS = [(dim, rope, at, heads) for dim, rope, at, heads in [
+    (128, 128, 0, 3), (192, 192, 0, 1), (192, 128, 64, 5), (256, 192, 64, 2), (256, 256, 0, 1), (224, 128, 32, 70),
+    (64, 48, 16, 1), (96, 16, 72, 9), (96, 80, 8, 1), (128, 32, 40, 1), (128, 32, 96, 33), (256, 240, 16, 1), (160, 64, 8, 4),
+    (32, 16, 16, 300)]]
+
+
+@pytest.mark.parametrize("dim,rope,at,heads", TURNS)
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("bits", [8, 16])
+def test_heads_turns(dim, rope, at, heads, halves, bits):
+    """Rotated parts of every width and place, for one token, a few, and more than a workgroup's."""
+    for n in (1, 3, 150):
+        x, w, b, f, pos = _head_inputs(dim + rope + n, n, heads, dim, rope, "layer")
+        got = _run_heads(x, w, b, f, pos, hm.head_format(dim, rope, at, int(halves), hm.HS_NORM_LAYER, 1e-6), bits)
+        y, err = ref.head(x.double(), "layer", w, b, 1e-6, pos, f, at, rope, halves)
+        if bits == 16:
+            _check_bf16(got, y, err, f"n {n}")
+        else:
+            ref.check_quantised(got[0].view(torch.float8_e4m3fn), got[1], y, err, 8, f"n {n}")
+
+
+def test_heads_past_one_pass():
+    """More heads than workgroups take in one pass, values past 4 GiB."""
+    n, heads, dim = 1_700_000, 40, 32
+    x = torch.zeros(n, heads, dim, dtype=torch.bfloat16, device="cuda")
+    pick = [0, 1, n // 2, n - 2, n - 1]
+    some, w, _, f, _ = _head_inputs(14, len(pick), heads, dim, 32, "rms")
+    x[pick] = some.cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    sw = _context()
+    for mode in (0, 1):
+        o = torch.zeros(n, heads, dim, dtype=torch.uint8, device="cuda")
+        s = torch.zeros(n, heads, 1, dtype=torch.uint8, device="cuda")
+        hm.hs_norm_rotate(sw.ctx, hm.head_format(dim, 32, 0, mode, hm.HS_NORM_RMS, 1e-6), x, w.cuda(), None, f.cuda(), pos,
+                          o.view(torch.float8_e4m3fn), scales=s)
+        y, err = ref.head(some.double(), "rms", w, None, 1e-6, torch.tensor(pick), f, 0, 32, bool(mode))
+        ref.check_quantised(o[pick].cpu().view(torch.float8_e4m3fn), s[pick].cpu(), y, err, 8, "o")
+        o[pick] = 0  # (the rest are zeros of either sign: a zero times a negative cosine is -0)
+        assert int(o.bitwise_and_(0x7F).count_nonzero()) == 0 and int((s == 27).sum()) >= (n - len(pick)) * heads
+
+
 def test_heads_strides():
     """Tokens and heads of any strides, transposed ones and the columns of a wider row, in and out; a call in place."""
     n, heads, dim = 19, 6, 64
@@ -420,6 +461,49 @@ def test_scores_not_numbers(bits, heads):
     assert torch.isnan(scores[1]).all() and torch.equal(scores.cpu()[[0, 2]], clean[[0, 2], :200])
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("heads", [16, 40])
+def test_scores_many_tokens(bits, heads):
+    """More tokens than are shared out evenly, alone in their groups (a token for each of many requests) and in groups of a
+    request, with skipped ones among them."""
+    gen = torch.Generator().manual_seed(heads)
+    for R, n in ((5000, 5000), (3, 9000)):
+        sw = _context(R, 90)
+        key = hm.key_format(64, hm.HS_KEY_MXFP8 if bits == 8 else hm.HS_KEY_MXFP4)
+        cache, codes, e, _ = _fill_cache(sw, key, gen)
+        q, qe, w = _queries(n, heads, 64, gen)
+        req = (torch.arange(n) * R // n).int()
+        pos = (torch.arange(n) * 7919 % 90).int()
+        req[::97], pos[::89] = -1, -1
+        scores = torch.full((n, 90), 77.0, device="cuda")
+        hm.hs_score_keys(sw.ctx, key, cache, q.cuda(), qe.cuda(), w.cuda(), req.cuda(), pos.cuda(), scores)
+        there = (req >= 0) & (pos >= 0)
+        assert (scores.cpu()[~there] == 77).all()
+        qd, keys = ref.decode(q.view(torch.uint8), qe, 8), ref.decode(codes, e, bits)[req.clamp(min=0).long()]
+        dots = torch.relu(qd @ keys.transpose(1, 2))
+        want = (w.double().unsqueeze(-1) * dots).sum(1)
+        size = (w.double().abs().unsqueeze(-1) * (qd.abs() @ keys.abs().transpose(1, 2))).sum(1)
+        seen = there[:, None] & (torch.arange(90) <= pos[:, None])
+        off = (scores.cpu().double() - want).abs()
+        assert (off <= size * (64 + heads + 4) * ref.F32 * 1.01 + 1e-37)[seen].all()
+        assert (scores.cpu()[there[:, None] & ~seen] == 77).all()
+
+
+def test_scores_short_contexts_of_long_caches():
+    """A cache of many positions of which few are filled, garbage (NaN bytes among it) behind them."""
+    gen = torch.Generator().manual_seed(6)
+    sw = _context(3, 200_000)
+    key = hm.key_format(128, hm.HS_KEY_MXFP8)
+    cache = torch.full((hm.hs_key_bytes(sw.cfg, key),), 0xFF, dtype=torch.uint8, device="cuda")
+    codes = (torch.randn(3, 50, 128, generator=gen) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    e = torch.randint(120, 132, (3, 50, 4), generator=gen, dtype=torch.uint8)
+    parts = hm.key_parts(sw.cfg, key, cache)
+    parts[0][:, :50] = codes.cuda()
+    parts[1][:, :50] = e.cuda()
+    q, qe, w = _queries(4, 32, 128, gen)
+    _check_scores(sw, key, cache, codes, e, 8, q, qe, w, [2, 0, 1, 2], [49, 0, 31, 12])
+
+
 def test_scores_repeat():
     """Equal inputs give equal bits, alone and in a batch."""
     gen = torch.Generator().manual_seed(5)
@@ -533,6 +617,47 @@ def test_select_by_request():
     _check_select(s, pos, 16, 0, cu=[0, 9, 12, 12], R=3)    # a request that ends past the tokens
     _check_select(s, pos, 16, 0, cu=[0, 0, 0, 0], R=3)
     _check_select(s, pos, 16, 0, cu=[0, 4, 2, 8], R=3)      # descending: not a batch's, no fault
+
+
+def test_select_many_rows():
+    """More rows than a launch takes, each of a few positions."""
+    rows, columns, k = (1 << 21) + 5, 8, 2
+    gen = torch.Generator().manual_seed(15)
+    s = torch.randn(rows, columns, generator=gen)
+    pos = (torch.arange(rows) % 9 - 1).int()
+    sw = _context(1, 1, k)
+    out = torch.full((rows, k), 77, dtype=torch.int32, device="cuda")
+    hm.hs_select(sw.ctx, s.cuda(), pos.cuda(), out)
+    masked = s.masked_fill(torch.arange(columns) > pos[:, None], -math.inf)
+    best, order = masked.sort(dim=1, descending=True, stable=True)
+    ids = torch.where(best[:, :k] > -math.inf, order[:, :k], columns).sort(dim=1).values
+    assert torch.equal(out.cpu(), torch.where(ids < columns, ids, -1).int())
+
+
+@pytest.mark.parametrize("columns,k", [(70_000, 2048), (300_000, 2048), (70_000, 5000)])
+def test_select_graph_of_long_rows(columns, k):
+    """Rows in several launches, captured once and replayed over other scores and lengths."""
+    rows = 2
+    sw = _context(rows, 1, k)
+    s = torch.zeros(rows, columns, device="cuda")
+    pos, out = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.zeros(rows, k, dtype=torch.int32, device="cuda")
+    work = sw.select_work(rows, columns)
+    hm.hs_select(sw.ctx, s, pos, out, recent=3, work=work)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hm.hs_select(sw.ctx, s, pos, out, recent=3, work=work)
+    gen = torch.Generator().manual_seed(16)
+    for i in range(4):
+        x = torch.randn(rows, columns, generator=gen)
+        lengths = [columns - 1 - i, [0, 100, columns // 2, -1][i]]
+        s.copy_(x)
+        pos.copy_(torch.tensor(lengths, dtype=torch.int32))
+        work.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        for r in range(rows):
+            assert out[r].tolist() == ref.select(x[r, :lengths[r] + 1], k, 3), f"replay {i}, row {r}"
 
 
 def test_select_random():
@@ -698,6 +823,62 @@ def test_offsets_past_32_bits():
     ids = torch.zeros(n, 2, dtype=torch.int32, device="cuda")
     hm.hs_select(sw.ctx, scores, where, ids, work=sw.select_work(n, H))
     assert ids[n - 1].tolist() == [5, H - 7]
+
+
+def test_refusals():
+    """What the library itself refuses: strides, alignment, sizes, formats, work buffers."""
+    sw = _context(2, 64, 4)
+    ctx, lib = sw.ctx, hm.lib()
+    x = torch.zeros(2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    flat = torch.zeros(100_000, dtype=torch.uint8, device="cuda")
+    f8 = lambda *n: torch.zeros(n, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)  # noqa: E731
+    ws, i2 = torch.zeros(2, 3, device="cuda"), _ints([0, 1])
+
+    def refused(msg, call):
+        with pytest.raises(hm.HiSparseError, match=msg) as e:
+            call()
+        assert e.value.code == hm.HS_E_INVALID
+
+    for bad, msg in (((48,), "dim"), ((288,), "dim"), ((0,), "dim"), ((64, 24), "rope"), ((64, 80), "rope"), ((64, -16), "rope"),
+                     ((64, 32, 4), "rope_at"), ((64, 32, 40), "rope_at"), ((64, 32, -8), "rope_at"), ((64, 32, 0, 2), "rope_style"),
+                     ((64, 32, 0, 0, 3), "norm"), ((64, 32, 0, 0, 1, -1.0), "eps"), ((64, 32, 0, 0, 1, math.inf), "eps"),
+                     ((64, 32, 0, 0, 1, math.nan), "eps")):
+        y = torch.zeros(1, 1, max(bad[0], 0), dtype=torch.bfloat16, device="cuda")
+        refused(msg, lambda: hm.hs_norm_rotate(ctx, hm.head_format(*bad), y, None, None, None, None, y))
+    one = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    refused("weight", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64), x, one, None, None, None, x))
+    refused("bias", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64, norm=1), x, one, one, None, None, x))
+    odd = torch.zeros(65, dtype=torch.bfloat16, device="cuda")[1:]
+    refused("aligned", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64, norm=1), x, odd, None, None, None, x))
+    wide = torch.zeros(2, 3, 68, dtype=torch.bfloat16, device="cuda")
+    refused("strides", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64), wide[..., :64], None, None, None, None, x))
+    refused("strides", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64), x, None, None, None, None, wide[..., :64]))
+    refused("strides", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64), x, None, None, None, None, x[:, :1].expand(2, 3, 64)))
+    refused("aligned", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64), x, None, None, None, None, f8(2, 3, 64),
+                                                 scales=flat[1:13].view(2, 3, 2)))
+    many = torch.zeros(1, 513, 64, dtype=torch.bfloat16, device="cuda")
+    refused("heads", lambda: hm.hs_norm_rotate(ctx, hm.head_format(64), many, None, None, None, None, many))
+    key = hm.key_format(64, hm.HS_KEY_MXFP8)
+    rows = x[:, 0]
+    refused("needs", lambda: hm.hs_store_keys(ctx, hm.head_format(64), key, rows, None, None, None, i2, i2, flat[:2 * 64 * 66 - 1]))
+    refused("aligned", lambda: hm.hs_store_keys(ctx, hm.head_format(64), key, rows, None, None, None, i2, i2, flat[8:]))
+    refused("dim", lambda: hm.hs_store_keys(ctx, hm.head_format(64), hm.key_format(128), rows, None, None, None, i2, i2, flat))
+    refused("x_stride", lambda: hm.hs_store_keys(ctx, hm.head_format(64), key, wide[:, 0, :64].view(2, 64)[:, :64].as_strided(
+        (2, 64), (68, 1)), None, None, None, i2, i2, flat))
+    s = torch.zeros(2, 64, device="cuda")
+    qs = torch.zeros(2, 3, 2, dtype=torch.uint8, device="cuda")
+    refused("needs", lambda: hm.hs_score_keys(ctx, key, flat[:100], f8(2, 3, 64), qs, ws, i2, i2, s))
+    refused("heads", lambda: hm.hs_score_keys(ctx, key, flat, f8(2, 65, 64), torch.zeros(2, 65, 2, dtype=torch.uint8, device="cuda"),
+                                              torch.zeros(2, 65, device="cuda"), i2, i2, s))
+    out = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    refused("recent", lambda: hm.hs_select(ctx, s, i2, out, recent=5))
+    refused("recent", lambda: hm.hs_select(ctx, s, i2, out, recent=-1))
+    refused("multiple of 4", lambda: hm.hs_select(ctx, torch.zeros(2, 63, device="cuda"), i2, out))
+    refused("aligned", lambda: hm.hs_select(ctx, torch.zeros(200, device="cuda")[1:129].view(2, 64), i2, out))
+    long = torch.zeros(2, 65536, device="cuda")
+    refused("work buffer", lambda: hm.hs_select(ctx, long, i2, out))
+    refused("work buffer", lambda: hm.hs_select(ctx, long, i2, out, work=flat[:hm.hs_select_work_bytes(sw.cfg, 2, 65536) - 1]))
+    assert lib.hs_score_keys(ctx, None, None, 0, None, None, 1, None, None, None, 0, None, 64, None) == hm.HS_E_INVALID
 
 
 def test_other_devices_and_contexts_are_refused():
