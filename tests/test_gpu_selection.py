@@ -634,7 +634,7 @@ def test_select_many_rows():
     assert torch.equal(out.cpu(), torch.where(ids < columns, ids, -1).int())
 
 
-@pytest.mark.parametrize("columns,k", [(70_000, 2048), (300_000, 2048), (70_000, 5000)])
+@pytest.mark.parametrize("columns,k", [(70_000, 2048), (300_000, 2048), (70_000, 5000), (500_000, 2048)])
 def test_select_graph_of_long_rows(columns, k):
     """Rows in several launches, captured once and replayed over other scores and lengths."""
     rows = 2
@@ -658,6 +658,101 @@ def test_select_graph_of_long_rows(columns, k):
         torch.cuda.synchronize()
         for r in range(rows):
             assert out[r].tolist() == ref.select(x[r, :lengths[r] + 1], k, 3), f"replay {i}, row {r}"
+
+
+def _long_rows(kind, columns, gen):
+    x = torch.randn(columns, generator=gen)
+    at = torch.arange(columns)
+    if kind == "up":
+        return at.float()
+    if kind == "down":
+        return -at.float()
+    if kind == "equal":
+        return torch.full((columns,), -2.5)
+    if kind == "two":
+        return (x > 0).float()
+    if kind == "few":  # fewer than are selected
+        return torch.where(at % 1000 == 7, x, -math.inf)
+    if kind == "nan":
+        return torch.where(at % 3 == 0, math.nan, torch.where(at % 7 == 0, -math.inf, x))
+    if kind == "infinite":
+        return torch.where(at % 31 == 0, math.inf, x)
+    if kind == "largest":
+        return torch.where(at % 2 == 0, 1.0, -1.0) * torch.finfo(torch.float32).max
+    if kind == "one part":
+        return torch.where((at >= 40_000) & (at < 47_000), x + 9, x)
+    if kind == "ties":
+        return x.mul(4).round()
+    if kind == "tiny":
+        return x * 1e-39
+    return x
+
+
+@pytest.mark.parametrize("kind", ["up", "down", "equal", "two", "few", "nan", "infinite", "largest", "one part", "ties", "tiny",
+                                  "normal"])
+@pytest.mark.parametrize("columns,k,recent", [(1_000_000, 2048, 64), (420_000, 2048, 0), (210_004, 4096, 4096), (640_000, 1300, 1)])
+def test_select_longest(kind, columns, k, recent):
+    """Rows whose parts' best do not fit one workgroup, with scores that leave little or most of them to be joined."""
+    gen = torch.Generator().manual_seed(columns + k)
+    rows = 3
+    s = torch.stack([_long_rows(kind, columns, gen) for _ in range(rows)])
+    pos = [columns - 1, columns // 3, columns - 4097]
+    sw = _context(rows, 1, k)
+    out = torch.full((rows, k), 77, dtype=torch.int32, device="cuda")
+    work = torch.full((hm.hs_select_work_bytes(sw.cfg, rows, columns) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    hm.hs_select(sw.ctx, s.cuda(), _ints(pos), out, recent=recent, work=work[:-64])
+    assert (work[-64:] == 0xFF).all()
+    for r in range(rows):
+        assert out[r].tolist() == ref.select(s[r, :pos[r] + 1], k, recent), f"row {r}"
+
+
+def test_select_longest_empty_rows_and_batches():
+    """Rows of no position, of one, of fewer than are selected, and requests' last tokens, in contexts of a million."""
+    columns, k = 1_000_000, 2048
+    gen = torch.Generator().manual_seed(17)
+    s = torch.randn(6, columns, generator=gen)
+    sw = _context(5, 1, k)
+    dev, work = s.cuda(), sw.select_work(6, columns)
+    for pos in ([-1, 0, 5, 2046, 2047, 2048], [16383, 16384, 49151, 49152, -1, 65535]):
+        out = torch.full((6, k), 77, dtype=torch.int32, device="cuda")
+        hm.hs_select(sw.ctx, dev, _ints(pos), out, recent=2, work=work)
+        for r in range(6):
+            assert out[r].tolist() == ref.select(s[r, :pos[r] + 1], k, 2), f"row {r}"
+    cu, pos = _ints([0, 2, 2, 3, 6, 6]), [9, 700_000, 3, 8, 99, 999_999]
+    out = torch.full((5, k), 77, dtype=torch.int32, device="cuda")
+    hm.hs_select(sw.ctx, dev, _ints(pos), out, cu=cu, recent=2, work=work)
+    for r, t in enumerate([1, None, 2, 5, None]):
+        want = [-1] * k if t is None else ref.select(s[t, :pos[t] + 1], k, 2)
+        assert out[r].tolist() == want, f"request {r}"
+
+
+def test_select_more_parts_than_are_joined():
+    columns, k = 17_000_000, 2048
+    gen = torch.Generator().manual_seed(18)
+    s = torch.randn(1, columns, generator=gen)
+    sw = _context(1, 1, k)
+    out = torch.full((1, k), 77, dtype=torch.int32, device="cuda")
+    hm.hs_select(sw.ctx, s.cuda(), _ints([columns - 1]), out, recent=1, work=sw.select_work(1, columns))
+    assert out[0].tolist() == ref.select(s[0], k, 1)
+
+
+def test_select_two_streams():
+    """Two calls at once, with a work buffer each."""
+    columns, k = 1_000_000, 2048
+    gen = torch.Generator().manual_seed(19)
+    s = torch.randn(2, 1, columns, generator=gen)
+    sw = _context(1, 1, k)
+    dev, streams = s.cuda(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    out = torch.full((2, 1, k), 77, dtype=torch.int32, device="cuda")
+    works = [sw.select_work(1, columns) for _ in range(2)]
+    pos = _ints([columns - 1])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            hm.hs_select(sw.ctx, dev[i], pos, out[i], recent=1, work=works[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert out[i, 0].tolist() == ref.select(s[i, 0], k, 1)
 
 
 def test_select_random():
