@@ -8,6 +8,9 @@
 // that take 8- and 4-bit operands as they are would spare that, but they lose of each sum what lies 2^-14 below its largest
 // product (normal keys and queries: 1.5e-5 off in 8 bits and 4e-6 in 4, 6e-9 in bf16), and the selection is made of these sums.
 // The queries of a workgroup's tokens lie in LDS as the instructions take them, and are read once for every 64 keys.
+// Memory bounds a token for each request (256 x 40960 keys x 32 heads in 4 bits 138 to 146 us, 4.7 to 5.0 TB/s; 32 ragged contexts x
+// 20 heads in 8 bits 16.6 us, 4.3 TB/s), the matrix units tokens in groups (4 x 128 tokens x 16000 keys x 32 heads 45 us, 940
+// TFLOP/s, 77 % of a large library product; relu and weights take vector instructions between).
 #include "hs_index.h"
 #include "hs_mfma.h"
 
@@ -18,7 +21,9 @@ namespace {
 constexpr int kScoreThreads = 256;
 constexpr int kScoreWaves = kScoreThreads / 64;
 constexpr int kJ = 2, kKeys = 32 * kJ;  // of a wave at a time
-constexpr int kMostGroups = 2048;       // whose keys are shared out evenly; more are taken one by one
+// Groups whose keys are shared out evenly; more are taken one by one, and the units even them out (32 requests x 16000 keys 15 us
+// evenly, 80 one by one; 256 x 4000 24 and 26; 2048 x 500 34 and 28, but there one long context among them would be left alone).
+constexpr int kMostGroups = 2048;
 constexpr int kMostBlocks = 1 << 20;
 
 // kRows: heads of a token filled up to 16, 32 or 64. kTokens: tokens of a workgroup.
@@ -233,14 +238,16 @@ __global__ __launch_bounds__(kScoreThreads, 2) void score_kernel(ScoreArgs a, in
           if (kParts > 1 && tile % kParts != kParts - 1) return;
 #pragma unroll
           for (int k = 0; k < (kRows == 16 && kTokens > 1 ? 2 : 1); ++k) {
-            const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[k][0]), __float_as_uint(sum[k][kJ - 1]), false, false);
+            const uint32_t u = __float_as_uint(sum[k][0]), v = __float_as_uint(sum[k][kJ - 1]);
+            const auto x = __builtin_amdgcn_permlane32_swap(u, v, false, false);
             const float all = __uint_as_float(x[0]) + __uint_as_float(x[1]);
             const int i = kRows == 16 ? tile * 2 + k : tile / kParts;
             int p = -1;
 #pragma unroll
             for (int j = 0; j < kTokens; ++j)
               if (j == i) p = last[j];
-            if (i >= begin && i < end && lane < kKeys && x0 + lane <= p - lo) a.scores[(int64_t)(t0 + i) * a.stride + lo + x0 + lane] = all;
+            if (i >= begin && i < end && lane < kKeys && x0 + lane <= p - lo)
+              a.scores[(int64_t)(t0 + i) * a.stride + lo + x0 + lane] = all;
           }
         };
         const int first = kTokens == 1 ? 0 : begin * kRows / 32, stop = kTokens == 1 ? kTiles : (end * kRows + 31) / 32;
@@ -248,8 +255,8 @@ __global__ __launch_bounds__(kScoreThreads, 2) void score_kernel(ScoreArgs a, in
 #pragma unroll 1
         for (int tile = first; tile < stop; ++tile) {
           int of = tile;
-          // (two tiles of one token: their queries are read when they are due, not kept in registers that spill: 256 requests x 2048
-          // keys x 64 heads in 8 bits 24.8 -> 18.8 us)
+          // (two tiles of one token: their queries are read when they are due, not kept in registers that spill: 256 requests x
+          // 2048 keys x 64 heads in 8 bits 24.8 -> 18.8 us)
           if (kRows > 32) asm volatile("" : "+s"(of));
           dots(of, acc);
           if (kRows > 32) __builtin_amdgcn_sched_barrier(0);
@@ -284,6 +291,9 @@ hipError_t launch(const ScoreArgs& a, hipStream_t s) {
 
 template <int kDim, bool kFour>
 hipError_t launch_heads_of(const ScoreArgs& a, hipStream_t s) {
+  // Tokens in groups of up to 8, which share their request's keys, where there are two for each of the context's requests (64
+  // requests x 8000 keys x 32 heads in 8 bits, us in groups / one by one: 1 token 19.7 / 15.5, 2 20.8 / 24.2, 4 26.4 / 42.8, 8
+  // 41.8 / 79.9)
   const bool many = a.n >= 2 * a.R;
   if (a.heads <= 16) return many ? launch<kDim, kFour, 16, 8>(a, s) : launch<kDim, kFour, 16, 1>(a, s);
   if (a.heads <= 32) return many ? launch<kDim, kFour, 32, 4>(a, s) : launch<kDim, kFour, 32, 1>(a, s);

@@ -3,7 +3,8 @@
 // A workgroup reads its part of a row once, into registers, 64 consecutive positions to a wave's load. What is selected is kept as
 // a mask of each such load, and a thread then writes the positions of one mask: passes over the registers are unrolled code that
 // runs once and waits for its own instructions, and three of them are enough (with two more, to count and to write by ballots,
-// 256 rows of 40960 took 31 us, with three 20). The k-th best score is found without a sort. It is no lower than the lowest of the threads' own
+// 256 rows of 40960 took 31 us, with three 20). The k-th best score is found without a sort. It is no lower than the lowest of the
+// threads' own
 // best scores (or second best, and so on: as many as make k); what lies above is counted in bins, even in value (which keeps a
 // wave's counts apart, where the bits of the scores would share few bins), and the scores of the one bin that the k-th lies in,
 // some dozens, are ranked against each other with their positions. A bin of more than kList (few different scores, or outliers
@@ -30,7 +31,8 @@ constexpr int kShortThreads = 512;
 constexpr int kShort = 8 * kShortThreads;
 constexpr int kList = 512;                   // scores of a bin that are ranked against each other
 constexpr int kMost = 48 * kSelectThreads;   // positions of a workgroup
-constexpr int kMiddle = 16 * kSelectThreads; // up to which a kernel that takes half of the registers is used
+constexpr int kMiddle = 16 * kSelectThreads; // of one that takes half of the registers
+constexpr int kUnits = 256;                  // of the card
 constexpr int kTopThreads = 256;
 constexpr int kEach = 32;                    // positions of a lane whose best is taken
 constexpr int kMostParts = kSelectThreads;   // that are joined
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(kThreads, kPer <= 16 ? 8 : 4) void select_kernel(Se
         hi = fmaxf(hi, highs[w]);
       }
       if (lo == -INFINITY) {
-        // too few scores for that bound: the lowest that may be selected, and how many may (a NaN becomes -infinity, so that no ballot
+        // too few scores for that bound: the lowest that may be selected, and how many may (a NaN becomes -inf, so that no ballot
         // meets one)
         int valid = 0;
         lo = INFINITY;
@@ -555,7 +557,8 @@ __global__ __launch_bounds__(kThreads, kPer <= 16 ? 8 : 4) void select_kernel(Se
       }
     }
     if (whole)
-      for (int i = all + tid; i < a.k; i += kThreads) a.topk[row * a.k + i] = i < all + recent ? (int32_t)(m - recent + i - all) : -1;
+      for (int i = all + tid; i < a.k; i += kThreads)
+        a.topk[row * a.k + i] = i < all + recent ? (int32_t)(m - recent + i - all) : -1;
     break;
   }
 }
@@ -643,8 +646,10 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t s) {
     const int64_t left = (int64_t)l.parts * a.k, most = l.n_in < l.part ? l.n_in : l.part;  // of a workgroup
     l.out = last ? nullptr : (float*)work;
     l.out_idx = (int32_t*)(work + (uint64_t)a.rows * left * 4);
+    // (the smaller kernels where they do: 256 rows of 4096 in 7.5 us, 9.4 with the next, 2048 of 8192 in 45, 60 with the next;
+    // but a workgroup that has a unit to itself may as well have all of its registers: 256 rows of 16384 11.4 -> 10.5)
     if (most <= kShort) launch<kShortThreads, kShort / kShortThreads>(a, l, s);
-    else if (most <= kMiddle) launch<kSelectThreads, kMiddle / kSelectThreads>(a, l, s);
+    else if (most <= kMiddle && (int64_t)a.rows * l.parts > kUnits) launch<kSelectThreads, kMiddle / kSelectThreads>(a, l, s);
     else launch<kSelectThreads, kMost / kSelectThreads>(a, l, s);
     if (last) return hipGetLastError();
     work += (uint64_t)a.rows * left * 8;
