@@ -8,9 +8,9 @@
 // that take 8- and 4-bit operands as they are would spare that, but they lose of each sum what lies 2^-14 below its largest
 // product (normal keys and queries: 1.5e-5 off in 8 bits and 4e-6 in 4, 6e-9 in bf16), and the selection is made of these sums.
 // The queries of a workgroup's tokens lie in LDS as the instructions take them, and are read once for every 64 keys.
-// Memory bounds a token for each request (256 x 40960 keys x 32 heads in 4 bits 138 to 146 us, 4.7 to 5.0 TB/s; 32 ragged contexts x
-// 20 heads in 8 bits 16.6 us, 4.3 TB/s), the matrix units tokens in groups (4 x 128 tokens x 16000 keys x 32 heads 45 us, 940
-// TFLOP/s, 77 % of a large library product; relu and weights take vector instructions between).
+// Memory bounds a token for each request (256 x 40960 keys x 32 heads in 4 bits 138 to 146 us, 4.7 to 5.0 TB/s; 32 ragged contexts
+// x 20 heads in 8 bits 16.6 us, 4.3 TB/s), the matrix units tokens in groups (4 x 128 tokens behind 3968 to 15872 keys x 32 heads 45
+// us, 940 TFLOP/s, 77 % of a large library product; relu and weights take vector instructions between).
 #include "hs_index.h"
 #include "hs_mfma.h"
 

@@ -4,18 +4,17 @@
 // a mask of each such load, and a thread then writes the positions of one mask: passes over the registers are unrolled code that
 // runs once and waits for its own instructions, and three of them are enough (with two more, to count and to write by ballots,
 // 256 rows of 40960 took 31 us, with three 20). The k-th best score is found without a sort. It is no lower than the lowest of the
-// threads' own
-// best scores (or second best, and so on: as many as make k); what lies above is counted in bins, even in value (which keeps a
-// wave's counts apart, where the bits of the scores would share few bins), and the scores of the one bin that the k-th lies in,
-// some dozens, are ranked against each other with their positions. A bin of more than kList (few different scores, or outliers
-// that stretch the range) is divided further, by the scores' bits, until kList are left or all are equal; the first of the
-// equal ones are then taken in order.
+// threads' own best scores (or second best, and so on: as many as make k); what lies above is counted in bins, even in value
+// (which keeps a wave's counts apart, where the bits of the scores would share few bins), and the scores of the one bin that the
+// k-th lies in, some dozens, are ranked against each other with their positions. A bin of more than kList (few different scores,
+// or outliers that stretch the range) is divided further, by the scores' bits, until kList are left or all are equal; the first
+// of the equal ones are then taken in order.
 // A row of more than kMost positions is cut into parts, whose best k (with their positions, in order) are the row of the next
 // launch; ties stay with the lowest positions, as every launch keeps the order. Where that would take a third launch, the first
 // one takes the best score of each of some thousand groups instead: the k-th best of those is a bound that k scores reach. A part
 // with no more than k of them leaves those (normal scores: 3000 of a million in all), one with more its best k, and one
 // workgroup joins them, 48 K at a time.
-// What bounds it: a row alone, the instructions and barriers of one workgroup (1 x 4096, k 256, 5.4 us); many rows, the vector
+// Bounded by: a row alone, the instructions and barriers of one workgroup (1 x 4096, k 256, 5.4 us); many rows, the vector
 // units, four passes of some instructions to a score (256 x 40960 18.8 us, 2.2 TB/s).
 #include "hs_index.h"
 
