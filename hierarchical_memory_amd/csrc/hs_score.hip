@@ -293,7 +293,7 @@ template <int kDim, bool kFour>
 hipError_t launch_heads_of(const ScoreArgs& a, hipStream_t s) {
   // Tokens in groups of up to 8, which share their request's keys, where there are two for each of the context's requests (64
   // requests x 8000 keys x 32 heads in 8 bits, us in groups / one by one: 1 token 19.7 / 15.5, 2 20.8 / 24.2, 4 26.4 / 42.8, 8
-  // 41.8 / 79.9)
+  // 41.8 / 79.9; a chunk of one request in a context of many pays for that: 128 tokens behind 16000 keys 26 / 41)
   const bool many = a.n >= 2 * a.R;
   if (a.heads <= 16) return many ? launch<kDim, kFour, 16, 8>(a, s) : launch<kDim, kFour, 16, 1>(a, s);
   if (a.heads <= 32) return many ? launch<kDim, kFour, 32, 4>(a, s) : launch<kDim, kFour, 32, 1>(a, s);
