@@ -194,6 +194,8 @@ _CTX_SIZES: Dict[int, _Limits] = {}
 
 
 def _ctx_key(ctx) -> int:
+    if type(ctx) is ctypes.c_void_p:
+        return ctx.value or 0
     if ctx is None:
         return 0
     return int(ctx.value or 0) if isinstance(ctx, ctypes.c_void_p) else int(ctx)
@@ -259,7 +261,7 @@ def _ptr(t) -> Optional[int]:
 
 
 def _bytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def hs_bind_device(ctx, hot, tail, slot_tok, stamp, lru_order, page, step, epoch) -> None:
@@ -731,14 +733,15 @@ def hs_score_keys(ctx, key: HsKeyFormat, keys, q, q_scales, weights, req, pos, s
     D = key.dim
     if q is None or scores is None:
         raise ValueError(f"{'q' if q is None else 'scores'} must not be None")
-    if q.dim() != 3 or q.shape[2] != D:
-        raise ValueError(f"q must have shape [n, heads, {D}], got {list(q.shape)}")
-    n, heads, _ = q.shape
-    if scores.dim() != 2 or scores.shape[0] != n or (lim is not None and scores.shape[1] < lim.H):
-        raise ValueError(f"scores must have shape [{n}, at least {lim.H if lim is not None else 'H'}], got "
-                         f"{list(scores.shape)}")
+    shape, rows = q.shape, scores.shape
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"q must have shape [n, heads, {D}], got {list(shape)}")
+    n, heads, _ = shape
+    if len(rows) != 2 or rows[0] != n or (lim is not None and rows[1] < lim.H):
+        raise ValueError(f"scores must have shape [{n}, at least {lim.H if lim is not None else 'H'}], got {list(rows)}")
+    columns = rows[1]
     step, one = scores.stride()
-    if one != 1 and scores.shape[1] > 1 or n > 1 and step < scores.shape[1]:
+    if one != 1 and columns > 1 or n > 1 and step < columns:
         raise ValueError("scores must have contiguous rows")
     dev = q.get_device()
     if not (q.dtype is f8 and q.is_contiguous() and _fine(q_scales, u8, (n, heads, D // 32), dev)
@@ -751,7 +754,7 @@ def hs_score_keys(ctx, key: HsKeyFormat, keys, q, q_scales, weights, req, pos, s
                 ("scores", scores[:0], f32, None, False))
     _check(lib().hs_score_keys(ctx, ctypes.byref(key), keys.data_ptr(), _bytes(keys), q.data_ptr(), q_scales.data_ptr(),
                                heads, weights.data_ptr(), req.data_ptr(), pos.data_ptr(), n, scores.data_ptr(),
-                               step if n > 1 else scores.shape[1], _raw_stream(stream, dev)))
+                               step if n > 1 else columns, _raw_stream(stream, dev)))
 
 
 def hs_select_work_bytes(cfg: HsConfig, rows: int, columns: int) -> int:
