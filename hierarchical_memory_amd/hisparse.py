@@ -462,6 +462,11 @@ def _at(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# Most tokens (or rows) of a call, as in the library. Counts past it are refused before they become int32 arguments: past 32
+# bits they would wrap into ones that the library takes.
+_MOST = 1 << 30
+
+
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
         return _torch._C._cuda_getCurrentRawStream(dev)
@@ -475,8 +480,8 @@ def hs_map_tokens(ctx, new, length, tail0, cu, req, pos, slot, status=None, stre
     lim = _CTX_SIZES.get(_ctx_key(ctx))
     R = lim.R if lim is not None else 0
     n = req.numel() if req is not None else 0
-    if n > 1 << 30:  # (as an int32 argument a length past 32 bits would wrap into one that the library takes)
-        raise ValueError(f"req, pos and slot must have at most {1 << 30} elements, got {n}")
+    if n > _MOST:
+        raise ValueError(f"req, pos and slot must have at most {_MOST} elements, got {n}")
     dev = new.get_device() if new is not None else -1
     if not (_i32_fine(new, R, dev) and _i32_fine(length, R, dev) and _i32_fine(cu, R + 1, dev)
             and _i32_fine(req, n, dev) and _i32_fine(pos, n, dev) and _i32_fine(slot, n, dev)
@@ -668,6 +673,8 @@ def hs_norm_rotate(ctx, fmt: HsHeadFormat, x, weight, bias, freqs, pos, o, scale
         raise ValueError(f"x must be a {bf16} tensor, got {x.dtype}")
     xt, xh = _strides("x", x, D)
     n, heads, _ = shape = x.shape
+    if n > _MOST or heads > _MOST:
+        raise ValueError(f"x must have at most {_MOST} tokens and heads, got {list(shape)}")
     if o.shape != shape:
         raise ValueError(f"o must have shape {list(shape)}, got {list(o.shape)}")
     dev = x.get_device()
@@ -706,6 +713,8 @@ def hs_store_keys(ctx, fmt: HsHeadFormat, key: HsKeyFormat, x, weight, bias, fre
     if x.dim() != 2 or x.shape[1] != D:
         raise ValueError(f"x must have shape [n, {D}], got {list(x.shape)}")
     n, (step, one) = x.shape[0], x.stride()
+    if n > _MOST:
+        raise ValueError(f"x must have at most {_MOST} tokens, got {list(x.shape)}")
     if one != 1:
         raise ValueError("x must have contiguous rows")
     dev = x.get_device()
@@ -737,6 +746,8 @@ def hs_score_keys(ctx, key: HsKeyFormat, keys, q, q_scales, weights, req, pos, s
     if len(shape) != 3 or shape[2] != D:
         raise ValueError(f"q must have shape [n, heads, {D}], got {list(shape)}")
     n, heads, _ = shape
+    if n > _MOST or heads > _MOST:
+        raise ValueError(f"q must have at most {_MOST} tokens and heads, got {list(shape)}")
     if len(rows) != 2 or rows[0] != n or (lim is not None and rows[1] < lim.H):
         raise ValueError(f"scores must have shape [{n}, at least {lim.H if lim is not None else 'H'}], got {list(rows)}")
     columns = rows[1]
@@ -759,6 +770,8 @@ def hs_score_keys(ctx, key: HsKeyFormat, keys, q, q_scales, weights, req, pos, s
 
 def hs_select_work_bytes(cfg: HsConfig, rows: int, columns: int) -> int:
     n = ctypes.c_uint64()
+    if abs(rows) >> 31 or abs(columns) >> 62:
+        raise ValueError(f"rows must be in [0, {_MOST}] and columns in [0, {1 << 31}], got {rows} and {columns}")
     _check(lib().hs_select_work_bytes(ctypes.byref(cfg), rows, columns, ctypes.byref(n)))
     return n.value
 
@@ -776,6 +789,10 @@ def hs_select(ctx, scores, pos, topk, cu=None, recent: int = 0, work=None, strea
     if scores.dim() != 2:
         raise ValueError(f"scores must have shape [n, columns], got {list(scores.shape)}")
     n, columns = scores.shape
+    if n > _MOST:
+        raise ValueError(f"scores must have at most {_MOST} rows, got {list(scores.shape)}")
+    if abs(recent) >> 31:
+        raise ValueError(f"recent must be in [0, {k}], got {recent}")
     step, one = scores.stride()
     if one != 1 and columns > 1:
         raise ValueError("scores must have contiguous rows")

@@ -136,3 +136,34 @@ def test_select_arguments(fake_ctx):
     _refused(lambda **a: hm.hs_select(fake_ctx, **a), good, bad)
     _refused(lambda **a: hm.hs_select(fake_ctx, **a), {**good, "cu": _i32(4), "topk": _i32(3, 8)},
              [("topk", _i32(2, 8), "topk has")])
+
+
+@pytest.mark.parametrize("n", [(1 << 30) + 1, 1 << 31, (1 << 32) + 4])
+def test_lengths_past_the_limit(fake_ctx, n):
+    """Refused by the tensors' shapes, also where 32 bits of a length would be one in range."""
+    meta = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    bf, i32, f32, f8 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn
+    fmt, key = hm.head_format(64), hm.key_format(64, hm.HS_KEY_MXFP8)
+    at, cache = meta(n, dtype=i32), _u8(100_000)
+    most = "at most 1073741824"
+    for shape in ((n, 1, 64), (2, n, 64)):
+        with pytest.raises(ValueError, match=most):
+            hm.hs_norm_rotate(fake_ctx, fmt, _bf(1, 1, 64).expand(shape), None, None, None, at, meta(*shape, dtype=bf))
+        with pytest.raises(ValueError, match=most):
+            hm.hs_score_keys(fake_ctx, key, cache, meta(*shape, dtype=f8), meta(*shape[:2], 2, dtype=torch.uint8),
+                             meta(*shape[:2], dtype=f32), at[:shape[0]], at[:shape[0]], meta(shape[0], 100, dtype=f32))
+    with pytest.raises(ValueError, match=most):
+        hm.hs_store_keys(fake_ctx, fmt, key, meta(n, 64, dtype=bf), None, None, None, at, at, cache)
+    for cu in (None, _i32(4)):
+        with pytest.raises(ValueError, match=most):
+            hm.hs_select(fake_ctx, meta(n, 4, dtype=f32), at, meta(n, 8, dtype=i32), cu=cu)
+
+
+def test_numbers_past_32_bits(fake_ctx):
+    cfg = hm.config(3, 8, 16, 0.0, 1152, 100, 4)
+    for rows, columns in (((1 << 32) + 4, 100), (-(1 << 32), 100), (4, (1 << 64) + 100)):
+        with pytest.raises(ValueError, match="rows must be in"):
+            hm.hs_select_work_bytes(cfg, rows, columns)
+    for recent in (1 << 32, -(1 << 32), (1 << 32) + 3):
+        with pytest.raises(ValueError, match="recent must be in"):
+            hm.hs_select(fake_ctx, torch.zeros(5, 100), _i32(5), _i32(5, 8), recent=recent)
