@@ -122,11 +122,17 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
         for (int i = 0; i < C; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum += y[i][e];
-        const float mean = quad_sum(sum) * kShare;
+        // The mean as the nearest 32 bits and what they leave of it: of values that hardly differ, next to nothing but that is
+        // left behind the mean (rows of equal values are zeros, as by the formula, and no noise over sqrt(eps)).
+        constexpr float kCount = 32 * C;
+        sum = quad_sum(sum);
+        float mean = sum * kShare;
+        mean = fmaf(fmaf(-kCount, mean, sum), kShare, mean);
+        const float rest = fmaf(-kCount, mean, sum) * kShare;
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[i][e] -= mean;
+          for (int e = 0; e < 8; ++e) y[i][e] = (y[i][e] - mean) - rest;
       }
       float sq = 0.0f;
 #pragma unroll

@@ -257,6 +257,44 @@ def test_heads_not_numbers(value):
     assert torch.isnan(y[1, 2]).any() and torch.isfinite(y[0]).all() and torch.isfinite(y[1, :2]).all()
 
 
+@pytest.mark.parametrize("dim", range(32, 257, 32))
+@pytest.mark.parametrize("bits", [8, 16])
+def test_layer_norm_of_equal_values(dim, bits):
+    """A row of equal values is its own mean: zeros, and the bias behind them, whatever the value and the number of them."""
+    v = torch.arange(0x3F80, 0x4000, dtype=torch.int16).view(torch.bfloat16).double()  # every mantissa
+    x = torch.cat([v * s for s in (1.0, 512.0, -2.0 ** -9, 2.0 ** 60)]).bfloat16()[:, None, None].expand(-1, 3, dim).contiguous()
+    b = (torch.arange(dim) % 7 - 3.0).bfloat16()
+    for bias in (None, b):
+        fmt = hm.head_format(dim, norm=hm.HS_NORM_LAYER, eps=1e-6)
+        got = _run_heads(x, None, bias, None, None, fmt, bits)
+        want = torch.zeros(dim) if bias is None else b.float()
+        if bits == 16:
+            assert torch.equal(got.float(), want.expand(got.shape))
+        else:
+            assert torch.equal(ref.decode(*got, 8).float(), want.expand(got[0].shape))
+
+
+@pytest.mark.parametrize("dim", [32, 96, 128, 160, 192, 224, 256])
+def test_layer_norm_of_nearly_equal_values(dim):
+    """Few values of a row one or two steps of bf16 off the others. The sum is exact in 32 bits (multiples of a step, no more
+    than 258 * 256 of them), values less their mean are too but for one rounding, and what is left are the roundings of the norm
+    itself: no share for the mean's."""
+    gen = torch.Generator().manual_seed(dim)
+    n = 400
+    m = 128 + torch.arange(n) % 127                                     # the mantissa, steps
+    steps = m[:, None, None] + (torch.rand(n, 2, dim, generator=gen) < 3 / dim) * torch.randint(1, 3, (n, 2, dim), generator=gen)
+    steps = steps.clamp(max=255)
+    x = (steps * 2.0 ** torch.tensor([2, -6])[torch.arange(n) % 2][:, None, None]).bfloat16()
+    for eps in (1e-6, 0.0):
+        got = _run_heads(x, None, None, None, None, hm.head_format(dim, norm=hm.HS_NORM_LAYER, eps=eps), 16)
+        v = x.double()
+        there = (steps.amax(-1) > steps.amin(-1)) if eps == 0 else torch.ones(n, 2, dtype=torch.bool)  # (0 / 0)
+        eps = float(torch.tensor(eps))  # as 32 bits hold it
+        c = v - v.mean(-1, keepdim=True)
+        y = c / torch.sqrt((c * c).mean(-1, keepdim=True) + eps)
+        _check_bf16(got[there], y[there], (y.abs() * (dim + 24) * ref.F32)[there], f"eps {eps}")
+
+
 # ---- key cache
 
 STORES = [(dim, bits, rope, norm, halves) for dim in (64, 128) for bits in (4, 8) for rope in (0, 32, 64)
