@@ -145,7 +145,8 @@ __global__ __launch_bounds__(kHeadThreads, kWavesOf(C)) void heads_kernel(HeadAr
       for (int i = 0; i < C; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[i][e] *= inv;
-      if (!(sq > 1e-28f && sq < 1e38f)) {  // squares that 32 bits lose (the four lanes take this branch, or none of them)
+      // squares that 32 bits lose, or their mean and an eps next to the largest (the four lanes take this branch, or none of them)
+      if (!(sq > 1e-28f && sq < 1e38f && a.eps < 1e38f)) {
         double m = 0.0, d = 0.0;
         const __bf16* again = (const __bf16*)in;  // (read again: registers are short)
         if (layer) {

@@ -217,6 +217,18 @@ def test_heads_magnitudes(norm, scale):
     _check_bf16(_run_heads(x, w, b, f, pos, fmt, 16), y, err + 1e-38, "o")
 
 
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 53, 2.0 ** 62])
+def test_heads_largest_eps(norm, scale):
+    """An eps that the mean of the squares lifts past 32 bits."""
+    x, w, b, f, pos = _head_inputs(21, 6, 3, 128, 64, norm)
+    x = (x.double() * scale).bfloat16()
+    eps = torch.finfo(torch.float32).max
+    y, err = ref.head(x.double(), norm, w, None, eps, pos, f, 0, 64, True)
+    got = _run_heads(x, w, None, f, pos, hm.head_format(128, 64, 0, 1, NORMS[norm], eps), 16)
+    _check_bf16(got, y, err, "o")
+
+
 @pytest.mark.parametrize("bits", [8, 16])
 def test_heads_rows_of_zeros(bits):
     x, w, b, f, pos = _head_inputs(4, 5, 2, 96, 32, "layer")
