@@ -17,6 +17,10 @@ typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 constexpr int kStatusBad = 1;  // HS_STATUS_BAD_ID
 constexpr int kHeadThreads = 256;
 constexpr int kMostHeadBlocks = 1 << 20;
+// Bytes of turns (and exchanged values) of a workgroup: with weight and bias the 64 KiB that a launch takes without a raised
+// limit. Only single heads of 256 values that are turned whole pass it in 64s, and go in 32s (40000 of them 27.1 us; with 240
+// values turned, in 64s, 26.1).
+constexpr size_t kMostTurns = (64 << 10) - 2 * 256 * sizeof(uint16_t);
 
 enum Out { kBf16, kMx8, kCache8, kCache4 };
 // How a rotated part in halves finds the other value of a pair, q = rope / 16 pieces of 8 values on: in the lane itself (q a
@@ -340,17 +344,20 @@ hipError_t launch(const HeadArgs& a, hipStream_t s) {
   // 256 tokens with 32 heads: 4.6 with 64, 5.3 with 16)
   int span = plan.mode == kAnywhere ? 16 : kHeadThreads / 4;
   auto tokens = [&] { return a.heads == 1 ? span : (a.heads + span - 2) / a.heads + 1; };
-  while (plan.mode != kStill && span > 4 && units < (int64_t)span * 512 && tokens() * (a.rope / 2) > kHeadThreads) span /= 2;
+  auto lds = [&] {
+    return plan.mode == kStill ? 0 : (size_t)tokens() * a.rope / 2 * sizeof(float2) +
+                                         (plan.mode == kAnywhere ? (size_t)span * a.rope * sizeof(float) : 0);
+  };
+  while (plan.mode != kStill && span > 4 &&
+         ((units < (int64_t)span * 512 && tokens() * (a.rope / 2) > kHeadThreads) || lds() > kMostTurns)) span /= 2;
   plan.span = span;
   plan.tokens = tokens();
-  const size_t lds = plan.mode == kStill ? 0 : (size_t)plan.tokens * a.rope / 2 * sizeof(float2) +
-                                                   (plan.mode == kAnywhere ? (size_t)span * a.rope * sizeof(float) : 0);
   const int64_t need = (units + span - 1) / span;
   const dim3 grid((uint32_t)(need < kMostHeadBlocks ? need : kMostHeadBlocks));
   if (plan.mode == kAnywhere || (plan.mode == kInLane && q > 4))
-    hipLaunchKernelGGL((heads_kernel<C, kOut, true>), grid, dim3(kHeadThreads), lds, s, a, plan);
+    hipLaunchKernelGGL((heads_kernel<C, kOut, true>), grid, dim3(kHeadThreads), lds(), s, a, plan);
   else
-    hipLaunchKernelGGL((heads_kernel<C, kOut, false>), grid, dim3(kHeadThreads), lds, s, a, plan);
+    hipLaunchKernelGGL((heads_kernel<C, kOut, false>), grid, dim3(kHeadThreads), lds(), s, a, plan);
   return hipGetLastError();
 }
 

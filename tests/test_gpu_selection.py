@@ -148,6 +148,29 @@ def test_heads_turns(dim, rope, at, heads, halves, bits):
             ref.check_quantised(got[0].view(torch.float8_e4m3fn), got[1], y, err, 8, f"n {n}")
 
 
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("dim,rope,heads", [(256, 256, 1), (256, 240, 1), (256, 256, 2)])
+def test_heads_many_turns(dim, rope, heads, halves, bits):
+    """Single heads turned whole, for more tokens than leave a workgroup few of them (their turns are its largest share of LDS):
+    as in small calls bit for bit, some of them against the model."""
+    n = 40_003
+    x, w, b, f, pos = _head_inputs(22, n, heads, dim, rope, "layer")
+    fmt = hm.head_format(dim, rope, 0, int(halves), hm.HS_NORM_LAYER, 1e-6)
+    got = _run_heads(x, w, b, f, pos, fmt, bits)
+    got = got if bits == 8 else (got,)
+    for t in (0, 20_000, n - 500):
+        few = _run_heads(x[t:t + 500], w, b, f, pos[t:t + 500], fmt, bits)
+        for g, m in zip(got, few if bits == 8 else (few,)):
+            assert torch.equal(g[t:t + 500].view(torch.uint8), m.view(torch.uint8))
+    pick = [0, 31, 32, 63, 64, n // 2, n - 2, n - 1]
+    y, err = ref.head(x[pick].double(), "layer", w, b, 1e-6, pos[pick], f, 0, rope, halves)
+    if bits == 16:
+        _check_bf16(got[0][pick], y, err, "o")
+    else:
+        ref.check_quantised(got[0][pick].view(torch.float8_e4m3fn), got[1][pick], y, err, 8, "o")
+
+
 def test_heads_past_one_pass():
     """More heads than workgroups take in one pass, values past 4 GiB."""
     n, heads, dim = 1_700_000, 40, 32
