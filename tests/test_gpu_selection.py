@@ -503,6 +503,38 @@ def test_scores_ranges(bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dim,heads", [(128, 20), (64, 3), (64, 40)])
+@pytest.mark.parametrize("copies", [1, 2])
+def test_scores_every_scale(bits, dim, heads, copies):
+    """Every scale byte but NaN's, 0 to 254: request b's keys have b, its queries 254 - b, and values that this keeps within
+    2^-126 and 2^128, where bf16 holds them exactly. One token for each request, and two (in groups)."""
+    gen = torch.Generator().manual_seed(heads + bits)
+    R, H = 255, 8
+    sw = _context(R, H)
+    key = hm.key_format(dim, hm.HS_KEY_MXFP8 if bits == 8 else hm.HS_KEY_MXFP4)
+
+    def codes_of(byte, count, kind):
+        grid = ref.grid_of(kind)
+        size = grid * 2.0 ** (byte - 127)
+        fine = ((size == 0) | ((size >= 2.0 ** -126) & (size < 2.0 ** 128))).nonzero()[:, 0]
+        code = fine[torch.randint(len(fine), (count,), generator=gen)]
+        return (code + torch.randint(2, (count,), generator=gen) * (128 if kind == 8 else 8)).to(torch.uint8)
+
+    c = torch.stack([codes_of(b, H * dim, bits).view(H, dim) for b in range(R)])
+    codes = c if bits == 8 else c[..., 0::2] | (c[..., 1::2] << 4)
+    e = torch.arange(R, dtype=torch.uint8)[:, None, None].expand(R, H, dim // 32).contiguous()
+    cache = sw.key_cache(key)
+    parts = hm.key_parts(sw.cfg, key, cache)
+    parts[0].copy_(codes)
+    parts[1].copy_(e)
+    req = [b for b in range(R) for _ in range(copies)]
+    q = torch.stack([codes_of(254 - b, heads * dim, 8).view(heads, dim) for b in req]).view(torch.float8_e4m3fn)
+    qe = (254 - torch.tensor(req)).to(torch.uint8)[:, None, None].expand(-1, heads, dim // 32).contiguous()
+    w = torch.randn(len(req), heads, generator=gen)
+    _check_scores(sw, key, cache, codes, e, bits, q, qe, w, req, [H - 1 - i % 3 for i in range(len(req))])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("heads", [1, 16, 64])
 def test_scores_not_numbers(bits, heads):
     """A NaN key makes its own scores NaN and no others; one behind a token's position, of another request, or in a NaN query
