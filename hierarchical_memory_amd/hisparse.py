@@ -819,6 +819,8 @@ def hs_destroy(ctx) -> None:
     if ctx:
         _CTX_SIZES.pop(_ctx_key(ctx), None)
         lib().hs_destroy(ctx)
+        if isinstance(ctx, ctypes.c_void_p):
+            ctx.value = None  # (whoever keeps this handle has none from here on: its calls are refused, not made of freed memory)
 
 
 class SwapIn:

@@ -1092,3 +1092,23 @@ def test_other_devices_and_contexts_are_refused():
     sw2.close()
     with pytest.raises(hm.HiSparseError):
         hm.hs_norm_rotate(None, hm.head_format(64), x, None, None, None, None, x)
+
+
+def test_closed_context_is_refused():
+    """Through a handle that was kept from before, by every call."""
+    sw = _context(2, 64, 4)
+    ctx = sw.ctx
+    key = hm.key_format(64, hm.HS_KEY_MXFP8)
+    cache, work = sw.key_cache(key), sw.select_work(2, 64)
+    x = torch.zeros(2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    q, qs = torch.zeros(2, 3, 64, dtype=torch.uint8, device="cuda"), torch.zeros(2, 3, 2, dtype=torch.uint8, device="cuda")
+    w, s, at = torch.zeros(2, 3, device="cuda"), torch.zeros(2, 64, device="cuda"), _ints([0, 1])
+    out = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    sw.close()
+    for call in (lambda: hm.hs_norm_rotate(ctx, hm.head_format(64), x, None, None, None, None, x),
+                 lambda: hm.hs_store_keys(ctx, hm.head_format(64), key, x[:, 0], None, None, None, at, at, cache),
+                 lambda: hm.hs_score_keys(ctx, key, cache, q.view(torch.float8_e4m3fn), qs, w, at, at, s),
+                 lambda: hm.hs_select(ctx, s, at, out, work=work)):
+        with pytest.raises(hm.HiSparseError, match="NULL") as e:
+            call()
+        assert e.value.code == hm.HS_E_INVALID

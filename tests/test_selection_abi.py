@@ -167,3 +167,18 @@ def test_numbers_past_32_bits(fake_ctx):
     for recent in (1 << 32, -(1 << 32), (1 << 32) + 3):
         with pytest.raises(ValueError, match="recent must be in"):
             hm.hs_select(fake_ctx, torch.zeros(5, 100), _i32(5), _i32(5, 8), recent=recent)
+
+
+def test_destroyed_handle_is_none(monkeypatch):
+    """The handle itself ends with its context, so that a copy of it reaches the library as NULL."""
+    seen = []
+
+    class Library:
+        hs_destroy = staticmethod(lambda ctx: seen.append(ctx.value))
+
+    ctx = ctypes.c_void_p(0x5EED3000)
+    copy = ctx
+    monkeypatch.setattr(hm.hisparse, "lib", lambda: Library)
+    for _ in range(2):
+        hm.hs_destroy(ctx)
+    assert seen == [0x5EED3000] and not copy.value
