@@ -567,6 +567,47 @@ def test_scores_not_numbers(bits, heads):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_stored_not_numbers_score_as_such(bits, dim, value):
+    """A key stored with a NaN or an infinity, whatever its other values (zeros among them), makes its scores NaN, whatever the
+    queries, and is never selected; its neighbours are scored and selected as without it."""
+    gen = torch.Generator().manual_seed(dim + bits)
+    n, heads, k = 40, 5, 8
+    sw = _context(1, n, k)
+    key = hm.key_format(dim, hm.HS_KEY_MXFP8 if bits == 8 else hm.HS_KEY_MXFP4)
+    x = torch.randn(n, dim, generator=gen).bfloat16()
+    bad = {3: 0, 17: dim // 2, 31: dim - 1, 39: 33}
+    x[17] = 0
+    at = torch.arange(n, dtype=torch.int32, device="cuda")
+    q = torch.randn(3, heads, dim, generator=gen).bfloat16()
+    q[2] = 0
+    q8 = torch.zeros(3, heads, dim, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    qs = torch.zeros(3, heads, dim // 32, dtype=torch.uint8, device="cuda")
+    hm.hs_norm_rotate(sw.ctx, hm.head_format(dim), q.cuda(), None, None, None, None, q8, scales=qs)
+    w = torch.ones(3, heads, device="cuda")
+    got = []
+    for with_them in (False, True):
+        if with_them:
+            for r, i in bad.items():
+                x[r, i] = value
+        cache = sw.key_cache(key)
+        hm.hs_store_keys(sw.ctx, hm.head_format(dim), key, x.cuda(), None, None, None, torch.zeros_like(at), at, cache)
+        scores = torch.full((3, n), 77.0, device="cuda")
+        hm.hs_score_keys(sw.ctx, key, cache, q8, qs, w, _ints([0] * 3), _ints([n - 1] * 3), scores)
+        ids = torch.zeros(3, k, dtype=torch.int32, device="cuda")
+        hm.hs_select(sw.ctx, scores, _ints([n - 1] * 3), ids)
+        got.append((scores.cpu(), ids.cpu()))
+    (clean, _), (scores, ids) = got
+    rows = list(bad)
+    assert torch.isnan(scores[:, rows]).all()
+    rest = [i for i in range(n) if i not in bad]
+    assert torch.equal(scores[:, rest], clean[:, rest])
+    for t in range(3):
+        assert ids[t].tolist() == ref.select(scores[t], k, 0) and not set(ids[t].tolist()) & set(rows)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("heads", [16, 40])
 def test_scores_many_tokens(bits, heads):
     """More tokens than are shared out evenly, alone in their groups (a token for each of many requests) and in groups of a
