@@ -3,8 +3,9 @@
 // Four lanes have a head, 8 values of every 32 each: a block under one scale is four lanes', a norm's sum takes two steps over
 // them, all of a lane's loads (16 bytes of each block) are on their way at once, and the pairs of a rotated part in halves that
 // is a multiple of 64 wide lie in one lane. A workgroup works out the turns (cosine and sine of its tokens' angles) while its
-// values come, once for all of a token's heads. Memory bounds many heads (8192 tokens x 16 heads x 192 values 23.7 us, 4.25 TB/s),
-// one workgroup's chain of reads, turns and norm few (256 x 32 x 128 4.7 us) and prompts' keys (41 K of 128 values 10.3 us).
+// values come, once for all of a token's heads. Memory bounds many heads (8192 tokens x 16 heads x 192 values 23.7 us, 4.25 TB/s,
+// where some of the inputs are still in the last-level cache, 25.9 us, 3.9 TB/s, where none are), one workgroup's chain of reads,
+// turns and norm few (256 x 32 x 128 4.7 us) and prompts' keys (41 K of 128 values 10.5 us).
 #include "hs_index.h"
 
 namespace hs {

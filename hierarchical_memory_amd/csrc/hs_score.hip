@@ -22,7 +22,8 @@ constexpr int kScoreThreads = 256;
 constexpr int kScoreWaves = kScoreThreads / 64;
 constexpr int kJ = 2, kKeys = 32 * kJ;  // of a wave at a time
 // Groups whose keys are shared out evenly; more are taken one by one, and the units even them out (32 requests x 16000 keys 15 us
-// evenly, 80 one by one; 256 x 4000 24 and 26; 2048 x 500 34 and 28, but there one long context among them would be left alone).
+// evenly, 80 one by one; 256 x 4000 24 and 26; 2048 x 500 34 and 28, but there one long context among them would be left alone, as
+// it is from 2049 groups on: their starts have to fit LDS).
 constexpr int kMostGroups = 2048;
 constexpr int kMostBlocks = 1 << 20;
 

@@ -13,9 +13,11 @@
 // launch; ties stay with the lowest positions, as every launch keeps the order. Where that would take a third launch, the first
 // one takes the best score of each of some thousand groups instead: the k-th best of those is a bound that k scores reach. A part
 // with no more than k of them leaves those (normal scores: 3000 of a million in all), one with more its best k, and one
-// workgroup joins them, 48 K at a time.
-// Bounded by: a row alone, the instructions and barriers of one workgroup (1 x 4096, k 256, 5.4 us); many rows, the vector
-// units, four passes of some instructions to a score (256 x 40960 18.8 us, 2.2 TB/s).
+// workgroup joins them, 48 K at a time. That is for k of up to 4096 (a quarter of a part) and rows of up to 16.7 M (the 1024 parts
+// that are joined); others go in as many launches of the first kind as they need.
+// Bounded by: a row alone, the instructions and barriers of one workgroup (1 x 4096, k 256, kernel 5.5 to 5.7 us); many rows, the
+// vector units, four passes of some instructions to a score (256 x 40960 18.5 to 19 us, 2.2 TB/s); the longest, three launches
+// (2 x 1 M 27 us), half of them the join, whose 48 scores to a thread do not fit its registers (66 spilled).
 #include "hs_index.h"
 
 #include <algorithm>
@@ -578,7 +580,8 @@ int64_t part_of(int k) { return 4 * k <= kMiddle ? kMiddle : kMost; }
 // Rows whose parts' best would not fit one workgroup are selected under a bound: the groups' best (k of them at least, with a
 // quarter to spare), from their k-th best on what a part has, joined. Three launches of which each takes little, against three
 // that each select k (2 rows x 1 M, k 2048, 34 -> 25 us, with many ties 40 -> 26; 16 rows x 400000 39 -> 32; 64 x 1 M 152 -> 136);
-// against two of those it is no gain (64 x 131072 31 -> 37 us, 1 x 1 M, k 256, 19.7 -> 22.3).
+// against two of those it is no gain (64 x 131072 31 -> 37 us, 1 x 1 M, k 256, 19.7 -> 22.3). A k past a quarter of a part would
+// leave too much of each, and parts are counted by a thread of the join each.
 struct Bounded {
   int64_t parts, chunks;
   int shift;
