@@ -621,14 +621,23 @@ def hs_attend_prompt(ctx, q, kv, rope, cu_q, cu_k, scale: float, o, lse=None, ca
                                   o.data_ptr(), _at(lse), _at(work), _bytes(work), _raw_stream(stream, dev)))
 
 
+def _int32(**numbers) -> None:
+    """Refuses what a format's 32-bit fields would take modulo 2^32."""
+    for name, v in numbers.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} must be a number of 32 bits, got {v}")
+
+
 def head_format(dim: int, rope: int = 0, rope_at: int = 0, rope_style: int = HS_ROPE_PAIRS, norm: int = HS_NORM_NONE,
                 eps: float = 0.0) -> HsHeadFormat:
     """How a head's vector is made: its values, the part of it that is rotated, its norm (HS_NORM_*)."""
+    _int32(dim=dim, rope=rope, rope_at=rope_at, rope_style=rope_style, norm=norm)
     return HsHeadFormat(dim, rope, rope_at, rope_style, norm, eps)
 
 
 def key_format(dim: int = 128, key_type: int = HS_KEY_MXFP8) -> HsKeyFormat:
     """Format of the index keys: values, HS_KEY_MXFP8 or HS_KEY_MXFP4."""
+    _int32(dim=dim, key_type=key_type)
     return HsKeyFormat(dim, key_type)
 
 

@@ -182,3 +182,14 @@ def test_destroyed_handle_is_none(monkeypatch):
     for _ in range(2):
         hm.hs_destroy(ctx)
     assert seen == [0x5EED3000] and not copy.value
+
+
+def test_formats_past_32_bits():
+    for name in ("dim", "rope", "rope_at", "rope_style", "norm"):
+        for v in ((1 << 32) + 32, -(1 << 32), 1 << 31):
+            with pytest.raises(ValueError, match=f"{name} must be a number of 32 bits"):
+                hm.head_format(**{"dim": 64, name: v})
+    for name in ("dim", "key_type"):
+        with pytest.raises(ValueError, match=f"{name} must be a number of 32 bits"):
+            hm.key_format(**{name: 1 << 32})
+    assert hm.head_format(-(1 << 31)).dim == -(1 << 31)  # (of 32 bits: the library's to refuse)
